@@ -1,7 +1,9 @@
 """AdaCluster clustered sparse attention on B200 (sm_100a).
 
 The compute path is libadacluster.so (include/adacluster.h); ``api.AdaCluster``
-is its Python front end.  ``workloads`` draws the seeded synthetic inputs.
+is its Python front end.  ``layer.AttnLayer`` fronts the calls around the
+attention: per-head norms with rotary positions, and a paged cache of keys and
+values with attention over it.  ``workloads`` draws the seeded synthetic inputs.
 """
 from . import workloads  # noqa: F401
 
@@ -18,4 +20,14 @@ def AdaCluster(*a, **k):  # noqa: N802 - thin alias that imports torch lazily
 
 def Config(*a, **k):  # noqa: N802
     from .api import Config as _C
+    return _C(*a, **k)
+
+
+def AttnLayer(*a, **k):  # noqa: N802
+    from .layer import AttnLayer as _L
+    return _L(*a, **k)
+
+
+def LayerConfig(*a, **k):  # noqa: N802
+    from .layer import LayerConfig as _C
     return _C(*a, **k)

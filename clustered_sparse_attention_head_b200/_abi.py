@@ -20,11 +20,17 @@ AC_F32, AC_BF16 = 0, 1
 AC_TAU_ABS, AC_TAU_MEAN_X, AC_TAU_MEDIAN_RADIUS_X = 0, 1, 2
 AC_FLAG_WARM_START, AC_FLAG_CHECK_FINITE, AC_FLAG_PROFILE, AC_FLAG_NO_GRAPH = 1, 2, 4, 8
 AC_SCORE_CENTROID, AC_SCORE_QUEST = 0, 1
+AC_NORM_NONE, AC_NORM_RMS, AC_NORM_LAYER = 0, 1, 2
+AC_ROPE_INTERLEAVED, AC_ROPE_HALF = 0, 1
+AC_ROPE_PLAIN, AC_ROPE_LINEAR, AC_ROPE_NTK, AC_ROPE_YARN = 0, 1, 2, 3
 
 # every entry point declared in include/adacluster.h
 EXPORTS = ["ac_create", "ac_destroy", "ac_capacities", "ac_workspace_size", "ac_cluster_q", "ac_cluster_k",
            "ac_select", "ac_select_rows", "ac_sparse_attn_rows", "ac_key_bounds", "ac_cluster_sort", "ac_cluster_sort_static", "ac_sparse_attn", "ac_forward", "ac_step_state_size", "ac_step_state_parts", "ac_forward_step",
-           "ac_profile_read", "ac_get_status", "ac_status_string", "ac_selftest_wait"]
+           "ac_profile_read", "ac_get_status", "ac_status_string", "ac_selftest_wait",
+           "ac_layer_create", "ac_layer_destroy", "ac_layer_workspace_size", "ac_layer_get_status",
+           "ac_rope_table_size", "ac_rope_table", "ac_qk_norm_rope", "ac_qk_norm_rope_backward",
+           "ac_cache_append", "ac_cache_attn"]
 
 
 class ac_config(ctypes.Structure):
@@ -48,6 +54,19 @@ class ac_profile(ctypes.Structure):
                 ("launches", ctypes.c_longlong)]
 
 
+class ac_layer_config(ctypes.Structure):
+    _fields_ = [("heads", c_int), ("kv_heads", c_int), ("d", c_int), ("dtype", c_int), ("w_dtype", c_int),
+                ("norm", c_int), ("eps", c_double), ("rope_axes", c_int), ("rope_dims", c_int * 3),
+                ("rope_max", c_int * 3), ("rope_layout", c_int), ("rope_theta", c_double), ("rope_scaling", c_int),
+                ("rope_factor", c_double), ("rope_orig", c_int), ("rope_beta_fast", c_double),
+                ("rope_beta_slow", c_double), ("page_size", c_int), ("causal_block", c_int), ("window", c_int),
+                ("scale", c_double)]
+
+
+class ac_tensor(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("token_stride", c_int64), ("head_stride", c_int64)]
+
+
 class AcError(RuntimeError):
     def __init__(self, fn, code, msg):
         super().__init__(f"{fn}: {msg} (status {code})")
@@ -65,7 +84,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"libadacluster.so not found at {path}; run __graft_entry__.build() first")
     lib = ctypes.CDLL(path)
-    P = c_void_p
+    P, T = c_void_p, POINTER(ac_tensor)
     sig = {
         "ac_create": ([POINTER(ac_config), POINTER(c_void_p)], c_int),
         "ac_destroy": ([P], None),
@@ -88,6 +107,17 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "ac_get_status": ([P, P], c_int),
         "ac_selftest_wait": ([P, c_double, P], c_int),
         "ac_status_string": ([c_int], ctypes.c_char_p),
+        "ac_layer_create": ([POINTER(ac_layer_config), POINTER(P)], c_int),
+        "ac_layer_destroy": ([P], None),
+        "ac_layer_workspace_size": ([P, POINTER(c_size_t)], c_int),
+        "ac_layer_get_status": ([P, P], c_int),
+        "ac_rope_table_size": ([P, POINTER(c_size_t)], c_int),
+        "ac_rope_table": ([P, P, P], c_int),
+        "ac_qk_norm_rope": ([P, c_int, c_int, P, P, c_int64, T, P, P, T, T, P, P, T, P], c_int),
+        "ac_qk_norm_rope_backward": ([P, c_int, c_int, P, P, c_int64, T, T, P, T, P, P, T, T, P, T, P, P, P, c_size_t,
+                                      P], c_int),
+        "ac_cache_append": ([P, c_int, c_int, P, P, P, c_int, c_int, P, P, T, P, P, T, P, P, T, P, P, T, P], c_int),
+        "ac_cache_attn": ([P, c_int, c_int, c_int, c_int, P, P, P, c_int, c_int, T, P, P, T, P, P, c_size_t, P], c_int),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)

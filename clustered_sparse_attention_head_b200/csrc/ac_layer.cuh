@@ -1,0 +1,102 @@
+// Internal interface of the calls around the attention (ac_layer_*): argument
+// blocks of the kernels in ac_rope.cu and ac_cache_attn.cu.
+#pragma once
+#include "ac_kernels.cuh"
+
+namespace ac {
+
+// [batch, token, head, d] view: data and strides in elements.
+struct View {
+    const void *p;
+    long long sb, sn, sh;
+};
+
+// Pair ranges and table offsets of the rotation's axes.
+struct RopeArgs {
+    int axes;             // 0 = no rotation
+    int pairs;            // R / 2
+    int half;             // layout
+    int first[3], np[3];  // first pair and number of pairs of each axis
+    int max[3];           // positions of each axis
+    long long off[3];     // first (cos, sin) of each axis in the table
+    long long cells;      // product of max: tokens of the implicit grid
+    const float2 *table;
+    const int32_t *pos;   // NULL: row-major coordinates of the token's index
+    long long pos_batch;  // elements between the samples' position blocks
+};
+
+enum { NORM_NONE = 0, NORM_RMS = 1, NORM_LAYER = 2 };
+
+// One tensor of the norm and rotation: x [token, head] rows to y.
+struct RowTensor {
+    View x, y;
+    const void *w, *b;  // [d] in the weights' type, or NULL
+    int heads;
+    int copy;           // 1: rows are copied (values on the way into the cache)
+    int paged;          // 1: y is a cache pool
+};
+
+// Where the new tokens of a paged cache go.
+struct PageArgs {
+    const int32_t *q_start, *kv_len, *block_table;
+    int seqs, max_pages, num_pages, page_log2, kv_heads;
+};
+
+struct RowArgs {
+    RowTensor t[3];
+    int nt;
+    int batch, n;      // tokens = batch * n rows of heads
+    int norm, w_f32;
+    float eps;
+    RopeArgs rope;
+    PageArgs page;     // seqs = 0: dense
+    int *status;
+};
+
+struct BackTensor {
+    View g, x, dx;
+    const void *w;
+    void *dw, *db;
+    int heads;
+};
+struct BackArgs {
+    BackTensor t[2];
+    int batch, n;
+    int norm, w_f32;
+    float eps;
+    RopeArgs rope;
+    int ctas[2];       // CTAs of each tensor
+    float *part;       // [ctas, 2, d] partial sums of dw and db
+    int *status;
+};
+
+// Freq of every pair (double) and the factor on cosine and sine.
+struct FreqArgs {
+    double f[64];
+    double mag;
+};
+
+// ---- ac_rope.cu
+void k_rope_table(const RopeArgs &r, const FreqArgs &f, float2 *table, cudaStream_t st);
+int k_norm_rope(const RowArgs &a, int dtype, int D, int num_sms, cudaStream_t st);
+// upper bound on ctas[0] + ctas[1] of k_norm_rope_back
+int back_ctas(int num_sms);
+int k_norm_rope_back(BackArgs &a, int dtype, int D, int num_sms, cudaStream_t st);
+
+// ---- ac_cache_attn.cu
+struct CacheAttnArgs {
+    int seqs, tokens, max_q, max_kv, heads, kv_heads, group, D;
+    int max_pages, num_pages, page_log2;
+    int causal_block, window;
+    float scale_log2;  // scale * log2(e)
+    const int32_t *q_start, *kv_len, *block_table;
+    View q, out;
+    const void *kp, *vp;
+    float *lse;
+    int *status;
+    void *ws;
+};
+size_t cache_attn_ws(int num_sms, int D);
+int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStream_t st);
+
+}  // namespace ac

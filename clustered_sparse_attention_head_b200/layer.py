@@ -1,0 +1,312 @@
+"""Python front end of the calls around the attention (ac_layer_*), with the
+same call names as the C ABI.
+
+``AttnLayer`` owns one ``ac_layer`` and a workspace.  It checks tensors' types,
+devices and shapes, takes views of any token and head strides (a slice of the
+packed projection needs no copy) and allocates outputs with torch; the work is
+the library's kernels.
+"""
+from __future__ import annotations
+
+import ctypes
+from ctypes import byref, c_void_p
+from dataclasses import dataclass
+
+import torch
+
+from . import _abi
+from ._abi import check
+
+_NORMS = {"none": _abi.AC_NORM_NONE, "rms": _abi.AC_NORM_RMS, "layer": _abi.AC_NORM_LAYER}
+_LAYOUTS = {"interleaved": _abi.AC_ROPE_INTERLEAVED, "half": _abi.AC_ROPE_HALF}
+_SCALINGS = {"none": _abi.AC_ROPE_PLAIN, "linear": _abi.AC_ROPE_LINEAR, "ntk": _abi.AC_ROPE_NTK,
+             "yarn": _abi.AC_ROPE_YARN}
+_DTYPES = {"bf16": (_abi.AC_BF16, torch.bfloat16), "f32": (_abi.AC_F32, torch.float32)}
+
+
+@dataclass
+class LayerConfig:
+    heads: int
+    d: int
+    kv_heads: int | None = None      # None: heads
+    dtype: str = "bf16"              # "bf16" | "f32"
+    w_dtype: str | None = None       # norm weights; None: dtype
+    norm: str = "rms"                # "none" | "rms" | "layer"
+    eps: float = 1e-6
+    rope_dims: tuple = ()            # rotated elements per axis; () = no rotation
+    rope_max: tuple = ()             # positions per axis (the latent grid)
+    rope_layout: str = "interleaved"  # | "half"
+    rope_theta: float = 10000.0
+    rope_scaling: str = "none"       # | "linear" | "ntk" | "yarn"
+    rope_factor: float = 1.0
+    rope_orig: int = 0
+    rope_beta_fast: float = 32.0
+    rope_beta_slow: float = 1.0
+    page_size: int = 0               # tokens per cache page; 0 = no cache
+    causal_block: int = 0            # 0: all keys; 1: causal by token; B: causal by blocks of B tokens
+    window: int = 0                  # > 0: only the last `window` positions
+    scale: float = 0.0               # 0: 1 / sqrt(d)
+
+    def __post_init__(self):
+        self.kv_heads = self.heads if self.kv_heads is None else self.kv_heads
+        self.w_dtype = self.w_dtype or self.dtype
+
+    def to_c(self) -> _abi.ac_layer_config:
+        def pick(table, key, what):
+            if key not in table:
+                raise ValueError(f"LayerConfig: {what} must be one of {sorted(table)}, not {key!r}")
+            return table[key]
+
+        if len(self.rope_dims) != len(self.rope_max) or len(self.rope_dims) > 3:
+            raise ValueError("LayerConfig: rope_dims and rope_max take one number per axis, at most three")
+        dims = (ctypes.c_int * 3)(*self.rope_dims)
+        top = (ctypes.c_int * 3)(*self.rope_max)
+        return _abi.ac_layer_config(
+            self.heads, self.kv_heads, self.d,
+            pick(_DTYPES, self.dtype, "dtype")[0], pick(_DTYPES, self.w_dtype, "w_dtype")[0],
+            pick(_NORMS, self.norm, "norm"), float(self.eps), len(self.rope_dims), dims, top,
+            pick(_LAYOUTS, self.rope_layout, "rope_layout"), float(self.rope_theta),
+            pick(_SCALINGS, self.rope_scaling, "rope_scaling"), float(self.rope_factor), int(self.rope_orig),
+            float(self.rope_beta_fast), float(self.rope_beta_slow), self.page_size, self.causal_block, self.window,
+            float(self.scale))
+
+
+class AttnLayer:
+    """One attention layer's calls.  ``device``: the GPU of every tensor passed
+    in.  Calls that use the workspace (ac_qk_norm_rope_backward, ac_cache_attn)
+    must not overlap on the GPU with another such call of the same layer."""
+
+    def __init__(self, cfg: LayerConfig, device="cuda", workspace: torch.Tensor | None = None):
+        self.cfg = cfg
+        self._layer = c_void_p()
+        self.lib = _abi.load()
+        device = torch.device(device)
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device.index is None else device
+        c = cfg.to_c()
+        with torch.cuda.device(self.device):
+            check("ac_layer_create", self.lib.ac_layer_create(byref(c), byref(self._layer)))
+        self.heads, self.kv_heads, self.d, self.axes = c.heads, c.kv_heads, c.d, c.rope_axes
+        self.dtype, self.w_dtype = _DTYPES[cfg.dtype][1], _DTYPES[cfg.w_dtype][1]
+        nb = ctypes.c_size_t()
+        check("ac_layer_workspace_size", self.lib.ac_layer_workspace_size(self._layer, byref(nb)))
+        self.ws_bytes = nb.value
+        if workspace is None:
+            workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("AttnLayer: workspace must be a contiguous tensor on the layer's device")
+        self.ws = workspace
+        self._ws_have = workspace.numel() * workspace.element_size()
+
+    def close(self):
+        if self._layer:
+            self.lib.ac_layer_destroy(self._layer)
+            self._layer = c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    # --------------------------------------------------------------- helpers
+    def _view(self, t, name, lead, heads):
+        """ac_tensor of a [*lead, heads, d] view; lead is (batch, tokens) or (tokens,)."""
+        if t.dtype != self.dtype or t.device != self.device:
+            raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {self.dtype} on {self.device}")
+        if tuple(t.shape) != (*lead, heads, self.d):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, self.d)}")
+        s = t.stride()
+        if s[-1] != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        return _abi.ac_tensor(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+
+    def _plain(self, t, name, dtype, shape):
+        """Pointer of a contiguous tensor (None: NULL)."""
+        if t is None:
+            return None
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {shape} "
+                             f"on {self.device}")
+        return t.data_ptr()
+
+    def _w(self, t, name):
+        return self._plain(t, name, self.w_dtype, (self.d,))
+
+    def _table(self, t):
+        if t is None:
+            if self.axes:
+                raise ValueError("table: this layer rotates, pass the tensor of ac_rope_table()")
+            return None
+        nb = ctypes.c_size_t()
+        check("ac_rope_table_size", self.lib.ac_rope_table_size(self._layer, byref(nb)))
+        return self._plain(t, "table", torch.float32, (nb.value // 8, 2))
+
+    def _pos(self, t, batch, n):
+        """Pointer and batch stride of [n, axes] or [batch, n, axes] positions."""
+        if t is None:
+            return None, 0
+        if t.dim() == 3:
+            return self._plain(t, "pos", torch.int32, (batch, n, self.axes)), n * self.axes
+        return self._plain(t, "pos", torch.int32, (n, self.axes)), 0
+
+    def _call(self, fn, stream, tensors, *args):
+        """The C call on `stream` (default: the current stream of the layer's
+        device).  Tensors used on another stream than the current one are
+        recorded there, so that freeing them does not hand their memory out
+        while the call runs."""
+        with torch.cuda.device(self.device):
+            current = torch.cuda.current_stream()
+            if stream is None:
+                stream = current
+            elif stream != current:
+                for t in tensors:
+                    if t is not None:
+                        t.record_stream(stream)
+            check(fn, getattr(self.lib, fn)(self._layer, *args, stream.cuda_stream))
+
+    def get_status(self, stream=None) -> int:
+        with torch.cuda.device(self.device):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            return self.lib.ac_layer_get_status(self._layer, s.cuda_stream)
+
+    # ------------------------------------------------------------- the calls
+    def ac_rope_table(self, stream=None):
+        """The layer's cosines and sines, [pairs of all axes, 2] fp32: made once,
+        passed to the calls below."""
+        nb = ctypes.c_size_t()
+        check("ac_rope_table_size", self.lib.ac_rope_table_size(self._layer, byref(nb)))
+        table = torch.empty(nb.value // 8, 2, dtype=torch.float32, device=self.device)
+        self._call("ac_rope_table", stream, (table,), table.data_ptr())
+        return table
+
+    def ac_qk_norm_rope(self, q, k, table=None, pos=None, w_q=None, w_k=None, b_q=None, b_k=None, q_out=None,
+                        k_out=None, stream=None):
+        """Norm and rotation of q [batch, n, heads, d] and k [batch, n, kv_heads, d]
+        (views of any strides; either may be None).  Returns (q_out, k_out) in
+        the attention's layout [batch, heads, n, d] unless given; given outputs
+        are [batch, heads, n, d] views too, and q_out = q.transpose(1, 2) works
+        in place."""
+        ref = q if q is not None else k
+        if ref is None or ref.dim() != 4:
+            raise ValueError("ac_qk_norm_rope: q or k [batch, n, heads, d] is required")
+        batch, n = ref.shape[:2]
+        table_p = self._table(table)
+        pos_p, pos_stride = self._pos(pos, batch, n)
+        args, outs = [], []
+        for x, w, b, y, heads, name in ((q, w_q, b_q, q_out, self.heads, "q"), (k, w_k, b_k, k_out, self.kv_heads, "k")):
+            if x is None:
+                if y is not None:
+                    raise ValueError(f"{name}_out without {name}")
+                args += [None, None, None, None]
+            else:
+                xv = self._view(x, name, (batch, n), heads)
+                if y is None:
+                    y = torch.empty(batch, heads, n, self.d, dtype=self.dtype, device=self.device)
+                args += [byref(xv), self._w(w, "w_" + name), self._w(b, "b_" + name),
+                         byref(self._view(y.transpose(1, 2), name + "_out", (batch, n), heads))]
+            outs.append(y)
+        self._call("ac_qk_norm_rope", stream, (q, k, table, pos, w_q, w_k, b_q, b_k, *outs), batch, n, table_p, pos_p,
+                   pos_stride, *args)
+        return tuple(outs)
+
+    def ac_qk_norm_rope_backward(self, gq, gk, q=None, k=None, table=None, pos=None, w_q=None, w_k=None, b_q=None,
+                                 b_k=None, dq=None, dk=None, stream=None):
+        """Gradients of ac_qk_norm_rope: gq [batch, heads, n, d], gk [batch,
+        kv_heads, n, d] and the forward call's inputs.  Returns a dict: "q", "k"
+        [batch, n, heads, d] (dq, dk if given), "w_q", "b_q", "w_k", "b_k" (None
+        where the forward call had no such weight)."""
+        ref = gq if gq is not None else gk
+        if ref is None or ref.dim() != 4:
+            raise ValueError("ac_qk_norm_rope_backward: gq or gk [batch, heads, n, d] is required")
+        batch, n = ref.shape[0], ref.shape[2]
+        norm = self.cfg.norm != "none"
+        table_p = self._table(table)
+        pos_p, pos_stride = self._pos(pos, batch, n)
+        args, res, used = [], {}, []
+        for g, x, w, b, dx, heads, name in ((gq, q, w_q, b_q, dq, self.heads, "q"),
+                                            (gk, k, w_k, b_k, dk, self.kv_heads, "k")):
+            dw = db = None
+            if g is None:
+                if dx is not None:
+                    raise ValueError(f"d{name} without g{name}")
+                args += [None] * 6
+            else:
+                if norm and x is None:
+                    raise ValueError(f"{name}: the norm's gradient needs the forward call's input")
+                gv = self._view(g.transpose(1, 2), "g" + name, (batch, n), heads)
+                if dx is None:
+                    dx = torch.empty(batch, n, heads, self.d, dtype=self.dtype, device=self.device)
+                if norm:
+                    xv = byref(self._view(x, name, (batch, n), heads))
+                    dw, db = (None if p is None else torch.empty(self.d, dtype=self.w_dtype, device=self.device)
+                              for p in (w, b))
+                else:
+                    xv = None
+                args += [byref(gv), xv, self._w(w, "w_" + name), byref(self._view(dx, "d" + name, (batch, n), heads)),
+                         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr()]
+                self._w(b, "b_" + name)
+            res.update({name: dx, "w_" + name: dw, "b_" + name: db})
+            used += [g, x, w, dx, dw, db]
+        self._call("ac_qk_norm_rope_backward", stream, (*used, table, pos, self.ws), batch, n, table_p, pos_p,
+                   pos_stride, *args, self.ws.data_ptr(), self._ws_have)
+        return res
+
+    def _cache(self, tokens, k_pages, v_pages, block_table, q_start, kv_len):
+        """The arguments that both cache calls share."""
+        seqs = kv_len.shape[0]
+        num_pages = k_pages.shape[0]
+        pool = (num_pages, self.kv_heads, self.cfg.page_size, self.d)
+        if block_table.dim() != 2:
+            raise ValueError("block_table: [sequences, pages] is required")
+        max_pages = block_table.shape[1]
+        return (seqs, tokens, self._plain(q_start, "q_start", torch.int32, (seqs + 1,)),
+                self._plain(kv_len, "kv_len", torch.int32, (seqs,)),
+                self._plain(block_table, "block_table", torch.int32, (seqs, max_pages)), max_pages, num_pages,
+                self._plain(k_pages, "k_pages", self.dtype, pool), self._plain(v_pages, "v_pages", self.dtype, pool))
+
+    def ac_cache_append(self, k, v, k_pages, v_pages, block_table, q_start, kv_len, q=None, table=None, pos=None,
+                        w_q=None, w_k=None, b_q=None, b_k=None, q_out=None, stream=None):
+        """Writes the new tokens' keys (normed, rotated) and values [tokens,
+        kv_heads, d] to their pages; with q [tokens, heads, d] returns the normed
+        and rotated queries (q_out if given), else None."""
+        tokens = k.shape[0]
+        seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
+                                                                        q_start, kv_len)
+        table_p = self._table(table)
+        pos_p = self._plain(pos, "pos", torch.int32, (tokens, self.axes))
+        qv = qo = None
+        if q is not None:
+            qv = byref(self._view(q, "q", (tokens,), self.heads))
+            if q_out is None:
+                q_out = torch.empty(tokens, self.heads, self.d, dtype=self.dtype, device=self.device)
+            qo = byref(self._view(q_out, "q_out", (tokens,), self.heads))
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self._call("ac_cache_append", stream,
+                   (k, v, k_pages, v_pages, block_table, q_start, kv_len, q, table, pos, w_q, w_k, b_q, b_k, q_out),
+                   seqs, tokens, qs, kl, bt, max_pages, num_pages, table_p, pos_p,
+                   byref(self._view(k, "k", (tokens,), self.kv_heads)), self._w(w_k, "w_k"), self._w(b_k, "b_k"),
+                   byref(self._view(v, "v", (tokens,), self.kv_heads)), kp, vp, qv, self._w(w_q, "w_q"),
+                   self._w(b_q, "b_q"), qo)
+        return q_out
+
+    def ac_cache_attn(self, q, k_pages, v_pages, block_table, q_start, kv_len, max_q=None, max_kv=None, out=None,
+                      lse=False, stream=None):
+        """Attention of the new tokens q [tokens, heads, d] over the cache.
+        max_q, max_kv: bounds on any sequence's new tokens and length (default:
+        what the tensors' shapes allow); tight bounds let short batches use the
+        whole GPU.  Returns out [tokens, heads, d], with lse=True (out, lse
+        [tokens, heads] fp32)."""
+        tokens = q.shape[0]
+        seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
+                                                                        q_start, kv_len)
+        if out is None:
+            out = torch.empty(tokens, self.heads, self.d, dtype=self.dtype, device=self.device)
+        lse_t = torch.empty(tokens, self.heads, dtype=torch.float32, device=self.device) if lse else None
+        self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
+                   seqs, tokens, tokens if max_q is None else int(max_q),
+                   max_pages * self.cfg.page_size if max_kv is None else int(max_kv), qs, kl, bt, max_pages, num_pages,
+                   byref(self._view(q, "q", (tokens,), self.heads)), kp, vp,
+                   byref(self._view(out, "out", (tokens,), self.heads)), None if lse_t is None else lse_t.data_ptr(),
+                   self.ws.data_ptr(), self._ws_have)
+        return (out, lse_t) if lse else out

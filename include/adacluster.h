@@ -353,6 +353,182 @@ AC_API ac_status ac_get_status(ac_ctx *ctx, void *stream);
 
 AC_API const char *ac_status_string(ac_status s);
 
+/* ------------------------------------------------------------------------
+ * Around the attention: what a transformer block does to q, k and v before it,
+ * and attention over a cache of earlier tokens.
+ *
+ * An ac_layer describes one attention layer.  Its calls take their sizes per
+ * call (batch, tokens, sequences), so one layer serves chunks of any length.
+ *  - Status, workspace and stream rules as above: argument errors return
+ *    synchronously and launch nothing; errors found on the device (a position
+ *    outside its table, a page id outside the pool, a length beyond the block
+ *    table) are recorded in the layer's status word (ac_layer_get_status).
+ *  - The current device must be the one the layer was created on
+ *    (AC_ERR_INVALID_ARG otherwise).
+ *  - Calls that take a workspace must not overlap on the GPU with another call
+ *    that uses the same workspace; the calls without one may overlap.
+ *  - No call synchronises or allocates, so each can be captured into a CUDA
+ *    graph; everything that changes from step to step (lengths, positions,
+ *    block table) is read from device memory.
+ * ------------------------------------------------------------------------ */
+
+/* Norm of each head's d elements before weight w and bias b [d]:
+ *   RMS:   y = x / sqrt(mean(x^2) + eps) * w + b
+ *   LAYER: the same of x - mean(x)
+ *   NONE:  y = x (w and b are not used).                                    */
+typedef enum { AC_NORM_NONE = 0, AC_NORM_RMS = 1, AC_NORM_LAYER = 2 } ac_norm;
+
+/* Rotary positions.  The first R elements of a head (R = the sum of rope_dims)
+ * form R/2 pairs: elements (2i, 2i+1) INTERLEAVED, (i, i + R/2) HALF (R must
+ * then be a multiple of 16); the rest of the head is not rotated.  Axis 0 owns
+ * the first rope_dims[0]/2 pairs, axis 1 the next rope_dims[1]/2, and so on.
+ * Pair j of axis a turns by p_a * f_aj, p_a the token's position on that axis
+ * and f_aj = theta^(-2j / rope_dims[a]), scaled for long contexts by
+ *   LINEAR: f / factor;
+ *   NTK:    theta * factor^(D / (D - 2)) in place of theta, D = rope_dims[a] > 2;
+ *   YARN:   f (g + (1 - g) / factor), with g = clamp((t - beta_slow) /
+ *           (beta_fast - beta_slow), 0, 1) and t = orig f / (2 pi) the pair's
+ *           turns within the original context of `orig` positions; cosine and
+ *           sine are multiplied by 0.1 ln(factor) + 1
+ *           ("YaRN: Efficient Context Window Extension of Large Language
+ *           Models", Peng et al., arXiv 2309.00071, §3).                     */
+typedef enum { AC_ROPE_INTERLEAVED = 0, AC_ROPE_HALF = 1 } ac_rope_layout;
+typedef enum { AC_ROPE_PLAIN = 0, AC_ROPE_LINEAR = 1, AC_ROPE_NTK = 2, AC_ROPE_YARN = 3 } ac_rope_scaling;
+
+typedef struct {
+    int heads, kv_heads, d;  /* query heads, a multiple of kv_heads (query head h reads key
+                                head h / (heads / kv_heads)); d in {64, 128}              */
+    ac_dtype dtype;          /* element type of q, k, v, out and the cache                 */
+    ac_dtype w_dtype;        /* element type of norm weights and biases and their gradients */
+    ac_norm norm;
+    double eps;              /* >= 0                                                       */
+    int rope_axes;           /* 0 = no rotation, else 1 to 3                               */
+    int rope_dims[3];        /* rotated elements per axis: even, > 0, sum <= d             */
+    int rope_max[3];         /* positions per axis: 0 .. rope_max - 1                      */
+    ac_rope_layout rope_layout;
+    double rope_theta;       /* > 0                                                        */
+    ac_rope_scaling rope_scaling;
+    double rope_factor;      /* >= 1 (not read with PLAIN)                                 */
+    int rope_orig;           /* YARN: the original context, > 0                            */
+    double rope_beta_fast, rope_beta_slow;  /* YARN: beta_fast > beta_slow >= 0            */
+    int page_size;           /* cache: tokens per page, a power of two in [16, 1024]; 0 =
+                                no cache (the cache calls return AC_ERR_UNSUPPORTED)       */
+    int causal_block;        /* ac_cache_attn: 0 = every key of the sequence, B > 0 = the
+                                keys j with floor(j / B) <= floor(p / B) for a query at
+                                position p (B = 1: causal by token; B = a frame's tokens:
+                                causal by whole frames)                                    */
+    int window;              /* ac_cache_attn: > 0 = only keys j > p - window; 0 = no limit */
+    double scale;            /* ac_cache_attn: factor on q.k; 0 = 1 / sqrt(d)              */
+} ac_layer_config;
+
+/* A [batch, token, head, d] view of device memory: strides in elements, the d
+ * elements of a head contiguous.  `data` 16-byte aligned and every stride a
+ * multiple of 16 bytes (of a dimension longer than 1).  Calls on ragged
+ * sequences have no batch dimension and do not read batch_stride.             */
+typedef struct {
+    void *data;
+    int64_t batch_stride, token_stride, head_stride;
+} ac_tensor;
+
+typedef struct ac_layer ac_layer;
+
+/* Validates the configuration and allocates the layer's status block.  *out =
+ * NULL on error.                                                             */
+AC_API ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out);
+AC_API void ac_layer_destroy(ac_layer *layer);
+
+/* Bytes of workspace for the calls below that take one (one size for all). */
+AC_API ac_status ac_layer_workspace_size(const ac_layer *layer, size_t *bytes);
+
+/* Synchronise `stream`, return the first device-side error of the layer's
+ * calls since the last read (AC_OK if none) and clear it. */
+AC_API ac_status ac_layer_get_status(ac_layer *layer, void *stream);
+
+/* The table of cosines and sines that the calls below read: for each axis a,
+ * [rope_max[a], rope_dims[a] / 2] pairs (cos, sin) in fp32, one axis after the
+ * other.  Angles are formed and reduced in double.  ac_rope_table_size: its
+ * bytes.  Written once per layer and kept by the caller (16-byte aligned).
+ * AC_ERR_UNSUPPORTED when the layer has no rotation.                          */
+AC_API ac_status ac_rope_table_size(const ac_layer *layer, size_t *bytes);
+AC_API ac_status ac_rope_table(ac_layer *layer, float *table, void *stream);
+
+/* Norm and rotation of every query and key head in one pass:
+ *   q_out = turn(norm(q) w_q + b_q), k_out likewise.
+ * Positions: pos [n, rope_axes] int32, shared by the samples, or one such block
+ * per sample pos_batch_stride elements apart; a token with a negative
+ * coordinate is not rotated; a coordinate >= rope_max is clamped and recorded
+ * (AC_ERR_INVALID_ARG in the status word).  pos = NULL: token i has the
+ * row-major coordinates of i in the grid rope_max[0] x rope_max[1] x ..., and
+ * tokens behind the grid (text) are not rotated.
+ * q / q_out or k / k_out may both be NULL (that side is skipped).  w and b may
+ * be NULL (1 and 0).  An output may be its input (same data and strides) and
+ * must not overlap an input otherwise.  Statistics and rotation in fp32, one
+ * rounding at the end.                                                        */
+AC_API ac_status ac_qk_norm_rope(ac_layer *layer, int batch, int n, const float *table, const int32_t *pos,
+                                 int64_t pos_batch_stride, const ac_tensor *q, const void *w_q, const void *b_q,
+                                 const ac_tensor *q_out, const ac_tensor *k, const void *w_k, const void *b_k,
+                                 const ac_tensor *k_out, void *stream);
+
+/* Gradients of ac_qk_norm_rope: from gq, gk (the gradients of q_out, k_out) and
+ * the inputs q, k:
+ *   g' = turn back(g);  dw = sum g' * x^;  db = sum g';  e = g' w;
+ *   dx = r (e - x^ mean(e x^))                 (RMS; r = 1/sqrt(mean x^2 + eps))
+ *   dx = r (e - mean(e) - x^ mean(e x^))       (LAYER)
+ * with x^ the normalised input.  dq / dk as the inputs' views; dw, db [d] in
+ * w_dtype may be NULL (not computed), summed over samples, tokens and heads in
+ * fp32 in a fixed order (the same bits on every call of the same sizes on the
+ * same device).  With AC_NORM_NONE, q and k are not read and may be NULL, and dw
+ * and db must be NULL.  dq may be gq or q, dk gk or k (same data and strides).  */
+AC_API ac_status ac_qk_norm_rope_backward(ac_layer *layer, int batch, int n, const float *table, const int32_t *pos,
+                                          int64_t pos_batch_stride, const ac_tensor *gq, const ac_tensor *q,
+                                          const void *w_q, const ac_tensor *dq, void *dw_q, void *db_q,
+                                          const ac_tensor *gk, const ac_tensor *k, const void *w_k,
+                                          const ac_tensor *dk, void *dw_k, void *db_k, void *ws, size_t ws_bytes,
+                                          void *stream);
+
+/* The cache of a layer is two pools k_pages, v_pages [num_pages, kv_heads,
+ * page_size, d].  Position p of sequence s lies in page block_table[s, p /
+ * page_size] (block_table [seqs, max_pages] int32), row p % page_size.  The new
+ * tokens of all sequences are stacked: sequence s has the rows q_start[s] ..
+ * q_start[s + 1] - 1 (q_start [seqs + 1] int32, ascending, within [0, tokens]);
+ * kv_len [seqs] int32 is each sequence's length with its new tokens, so the
+ * new tokens stand at positions kv_len - (number of new tokens) .. kv_len - 1.
+ * Rows of the stacked tensors outside every sequence are left as they are.
+ *
+ * ac_cache_append writes the new tokens' keys, normed and turned as in
+ * ac_qk_norm_rope, and values to their places in the pools, and (q non-NULL)
+ * the queries, normed and turned, to q_out, in one launch.  A token's position
+ * is its place in the sequence, read as in ac_qk_norm_rope with pos = NULL, or
+ * pos [tokens, rope_axes].  A token whose page id is outside [0, num_pages) or
+ * whose place is outside the block table is not written to the cache, and
+ * AC_ERR_INVALID_ARG is recorded.  Two sequences that share a page being
+ * written race for it.                                                        */
+AC_API ac_status ac_cache_append(ac_layer *layer, int seqs, int tokens, const int32_t *q_start,
+                                 const int32_t *kv_len, const int32_t *block_table, int max_pages, int num_pages,
+                                 const float *table, const int32_t *pos, const ac_tensor *k, const void *w_k,
+                                 const void *b_k, const ac_tensor *v, void *k_pages, void *v_pages,
+                                 const ac_tensor *q, const void *w_q, const void *b_q, const ac_tensor *q_out,
+                                 void *stream);
+
+/* Exact softmax attention of the new tokens over their sequences' caches:
+ *   out_i = sum_j softmax_j(scale q_i.k_j) v_j
+ * over the keys j < kv_len[s] that causal_block and window leave to the query's
+ * position.  A query that sees no key gets zeros (lse -inf).  lse [tokens,
+ * heads] (natural-log log-sum-exp of the scaled scores) is written when
+ * non-NULL.  max_q and max_kv bound the new tokens and the length of any
+ * sequence: a sequence beyond its bound, or beyond the block table, is cut to
+ * it (its first max_q new tokens, its first max_kv keys) and AC_ERR_INVALID_ARG
+ * recorded; a page id outside the pool is clamped and recorded.  Cache rows at
+ * or beyond kv_len are never used, whatever they hold; rows before it must be
+ * finite (a NaN or Inf value may reach every query of its sequence).
+ * bf16 only (AC_ERR_UNSUPPORTED otherwise): products in bf16 with fp32
+ * accumulation, softmax in fp32, its weights rounded to bf16 for the product
+ * with v.                                                                     */
+AC_API ac_status ac_cache_attn(ac_layer *layer, int seqs, int tokens, int max_q, int max_kv, const int32_t *q_start,
+                               const int32_t *kv_len, const int32_t *block_table, int max_pages, int num_pages,
+                               const ac_tensor *q, const void *k_pages, const void *v_pages, const ac_tensor *out,
+                               float *lse, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
