@@ -407,6 +407,9 @@ ac_status ac_cache_attn(ac_layer *l, int seqs, int tokens, int max_q, int max_kv
     if (tokens && (!view_ok(*q, 1, tokens, hq, d, l->elt, false) || !view_ok(*out, 1, tokens, hq, d, l->elt, true) ||
                    !alias_ok(*q, *out, 1, tokens, hq, d, l->elt)))
         return AC_ERR_INVALID_ARG;
+    // query tiles are tensor-map boxes of whole groups
+    if (hq / l->cfg.kv_heads > 128 || (tokens > 1 && !q->token_stride) || (hq > 1 && !q->head_stride))
+        return AC_ERR_UNSUPPORTED;
     size_t need = 0;
     ac_layer_workspace_size(l, &need);
     if (!ws || !aligned16(ws) || ws_bytes < need) return AC_ERR_WORKSPACE;
