@@ -739,13 +739,6 @@ template <int D> int launch(const CacheAttnArgs &a, const Plan &pl, int num_sms,
     const cuuint64_t strides[1] = {(cuuint64_t)D * 2};
     const cuuint32_t box[2] = {64, (cuuint32_t)std::min(page, CHUNK)};
     if (!encode(encode_fn, &mk, kp, 2, dims, strides, box) || !encode(encode_fn, &mv, vp, 2, dims, strides, box)) return -1;
-    // the register split assumes the launch budget ptxas gave the kernel; a
-    // larger split would make setmaxnreg.inc wait forever, so refuse.  The
-    // shared-memory attribute belongs to the current device: set on every call.
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, cache_attn_kernel<D>) != cudaSuccess || fa.numRegs != C::REGS_LAUNCH) return -1;
-    if (cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return -1;
     cache_attn_kernel<D><<<std::min(pl.units, num_sms), C::NTHREADS, C::SMEM, st>>>(mq, mk, mv, a, pl);
     note_launch();
     if (pl.nsplit > 1) {
@@ -757,7 +750,21 @@ template <int D> int launch(const CacheAttnArgs &a, const Plan &pl, int num_sms,
     return 0;
 }
 
+// The register split assumes the launch budget ptxas gave the kernel; a larger
+// split would make setmaxnreg.inc wait forever, so refuse.
+template <int D> int setup() {
+    using C = CCfg<D>;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, cache_attn_kernel<D>) != cudaSuccess || fa.numRegs != C::REGS_LAUNCH) return -1;
+    return cudaFuncSetAttribute(cache_attn_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) ==
+                   cudaSuccess
+               ? 0
+               : -1;
+}
+
 }  // namespace
+
+int cache_attn_setup(int D) { return D == 64 ? setup<64>() : setup<128>(); }
 
 size_t cache_attn_ws(int num_sms, int D) {
     return (size_t)max_slots(num_sms) * 256 * (D * sizeof(float) + sizeof(float2));

@@ -138,8 +138,7 @@ ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out) {
             return AC_ERR_INVALID_ARG;
         f.mag = sc == AC_ROPE_YARN ? 0.1 * log(g.rope_factor) + 1.0 : 1.0;
         r.half = g.rope_layout == AC_ROPE_HALF;
-        r.cells = 1;
-        long long off = 0;
+        long long off = 0, cells = 1;
         for (int a = 0; a < r.axes; a++) {
             const int D = g.rope_dims[a];
             if (D < 2 || D > g.d || (D & 1) || g.rope_max[a] < 1 || (sc == AC_ROPE_NTK && D == 2))
@@ -147,10 +146,11 @@ ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out) {
             r.first[a] = r.pairs;
             r.np[a] = D / 2;
             r.max[a] = g.rope_max[a];
-            r.off[a] = off;
+            r.off[a] = (uint32_t)off;
             off += (long long)r.max[a] * r.np[a];
-            r.cells = std::min(r.cells * r.max[a], 1LL << 31);
+            cells = std::min(cells * r.max[a], 0x7fffffffLL);
             r.pairs += D / 2;
+            if (off > (1LL << 31)) return AC_ERR_UNSUPPORTED;  // a table of 16 GiB
             if (2 * r.pairs > g.d) return AC_ERR_INVALID_ARG;
             const double theta = sc == AC_ROPE_NTK ? g.rope_theta * pow(g.rope_factor, D / (D - 2.0)) : g.rope_theta;
             for (int j = 0; j < D / 2; j++) {
@@ -169,7 +169,9 @@ ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out) {
             r.first[a] = r.pairs;
             r.max[a] = 1;
         }
-        if (off > (1LL << 33)) return AC_ERR_UNSUPPORTED;  // a table of 64 GiB
+        r.cells = (int)cells;
+        r.by1 = FastDiv(r.max[1]);
+        r.by2 = FastDiv(r.max[2]);
         if (r.half && r.pairs % 8) return AC_ERR_UNSUPPORTED;
     }
     ac_layer *l = (ac_layer *)calloc(1, sizeof(ac_layer));
@@ -188,7 +190,8 @@ ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out) {
     cudaDriverEntryPointQueryResult qr;
     if (cudaMemset(l->d_status, 0, 8 * sizeof(int)) != cudaSuccess ||
         cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &l->encode_fn, cudaEnableDefault, &qr) != cudaSuccess ||
-        qr != cudaDriverEntryPointSuccess || !l->encode_fn) {
+        qr != cudaDriverEntryPointSuccess || !l->encode_fn ||
+        rope_setup(g.dtype, g.d, r.half, g.norm) || (g.page_size && g.dtype == AC_BF16 && cache_attn_setup(g.d))) {
         ac_layer_destroy(l);
         return AC_ERR_CUDA;
     }
@@ -264,6 +267,7 @@ ac_status ac_qk_norm_rope(ac_layer *l, int batch, int n, const float *table, con
     if (e != AC_OK || !batch || !n || !a.nt) return e;
     a.batch = batch;
     a.n = n;
+    a.by_n = FastDiv(n);
     a.norm = l->cfg.norm;
     a.w_f32 = l->cfg.w_dtype == AC_F32;
     a.eps = (float)l->cfg.eps;
@@ -326,6 +330,7 @@ ac_status ac_qk_norm_rope_backward(ac_layer *l, int batch, int n, const float *t
     }
     a.batch = batch;
     a.n = n;
+    a.by_n = FastDiv(n);
     a.norm = l->cfg.norm;
     a.w_f32 = l->cfg.w_dtype == AC_F32;
     a.eps = (float)l->cfg.eps;
@@ -386,6 +391,7 @@ ac_status ac_cache_append(ac_layer *l, int seqs, int tokens, const int32_t *q_st
     a.t[a.nt++] = RowTensor{view_of(*v), vp, nullptr, nullptr, hk, 1, 1};
     a.batch = 1;
     a.n = tokens;
+    a.by_n = FastDiv(tokens);
     a.norm = l->cfg.norm;
     a.w_f32 = l->cfg.w_dtype == AC_F32;
     a.eps = (float)l->cfg.eps;

@@ -11,6 +11,19 @@ struct View {
     long long sb, sn, sh;
 };
 
+// n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and m =
+// floor(2^32 (2^l - d) / d) + 1, n / d = (mulhi(n, m) + n) >> l (Granlund and
+// Montgomery, "Division by Invariant Integers using Multiplication", 1994).
+struct FastDiv {
+    uint32_t d, m, l;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d_) : d(d_), l(0) {
+        while ((1ull << l) < d) l++;
+        m = (uint32_t)((((1ull << l) - d) << 32) / d + 1);
+    }
+    __device__ __forceinline__ int div(int n) const { return (int)((__umulhi((uint32_t)n, m) + (uint32_t)n) >> l); }
+};
+
 // Pair ranges and table offsets of the rotation's axes.
 struct RopeArgs {
     int axes;             // 0 = no rotation
@@ -18,8 +31,9 @@ struct RopeArgs {
     int half;             // layout
     int first[3], np[3];  // first pair and number of pairs of each axis
     int max[3];           // positions of each axis
-    long long off[3];     // first (cos, sin) of each axis in the table
-    long long cells;      // product of max: tokens of the implicit grid
+    uint32_t off[3];      // first (cos, sin) of each axis in the table
+    int cells;            // product of max, at most 2^31 - 1: tokens of the implicit grid
+    FastDiv by1, by2;     // by max[1] and max[2]
     const float2 *table;
     const int32_t *pos;   // NULL: row-major coordinates of the token's index
     long long pos_batch;  // elements between the samples' position blocks
@@ -46,6 +60,7 @@ struct RowArgs {
     RowTensor t[3];
     int nt;
     int batch, n;      // tokens = batch * n rows of heads
+    FastDiv by_n;
     int norm, w_f32;
     float eps;
     RopeArgs rope;
@@ -62,10 +77,13 @@ struct BackTensor {
 struct BackArgs {
     BackTensor t[2];
     int batch, n;
+    FastDiv by_n;
     int norm, w_f32;
     float eps;
     RopeArgs rope;
     int ctas[2];       // CTAs of each tensor
+    int run;           // heads per item
+    FastDiv by_runs[2];  // by the items of a tile, per tensor
     float *part;       // [ctas, 2, d] partial sums of dw and db
     int *status;
 };
@@ -78,6 +96,8 @@ struct FreqArgs {
 
 // ---- ac_rope.cu
 void k_rope_table(const RopeArgs &r, const FreqArgs &f, float2 *table, cudaStream_t st);
+// the forward kernel's shared-memory attribute on the current device: once per layer
+int rope_setup(int dtype, int D, int half, int norm);
 int k_norm_rope(const RowArgs &a, int dtype, int D, int num_sms, cudaStream_t st);
 // upper bound on ctas[0] + ctas[1] of k_norm_rope_back
 int back_ctas(int num_sms);
@@ -96,6 +116,8 @@ struct CacheAttnArgs {
     int *status;
     void *ws;
 };
+// the kernel's attributes on the current device: once per layer
+int cache_attn_setup(int D);
 size_t cache_attn_ws(int num_sms, int D);
 int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStream_t st);
 

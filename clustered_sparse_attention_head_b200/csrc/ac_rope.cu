@@ -4,58 +4,94 @@
 // Row of a head: x [d] -> n = (x - [mean]) r, r = 1 / sqrt(mean(.^2) + eps)
 // -> n w + b -> pairs (a, b) turned by the token's angle:
 //    (a cos - b sin, a sin + b cos).
-// Bound by memory: each row is read once and written once, about 60
-// instructions per 16 bytes.  A group of G lanes (16 bytes each) holds one row
-// in registers, so the statistics are xor shuffles within the group; it keeps
-// one token's cosines, sines and the weights and takes HC heads of that token,
-// so the table's 8 bytes per pair are read once per HC rows and HC loads of 16
-// bytes are in flight per lane.
+// Bound by memory: each row is read once and written once.  A group of G lanes
+// (16 bytes each) holds one row in registers, so the statistics are xor shuffles
+// within the group.  It keeps one token and walks its heads, HC rows in flight,
+// with weight, bias, cosine and sine folded into coefficients once per token and
+// tensor: y = r (x ca + x' cb) + rb with x' the pair's other element, six
+// operations per element.
 #include "ac_layer.cuh"
+#include "ac_softmax.cuh"
 
 namespace ac {
 namespace {
 
 constexpr int NT = 256;
+constexpr int HS = 1;      // heads that a CTA's groups take side by side
+constexpr int FWD_HC = 8, FWD_STEPS = 2, FWD_CTAS = 3;
+constexpr int BACK_HC = 4, BACK_STEPS = 3, BACK_CTAS = 2, BACK_MOST = 32;
 
-// 16 bytes of a row as floats and back (round to nearest even).
+// Packed pairs of fp32: one instruction for two elements.  The forward kernel
+// runs at the memory's rate only with fewer than ~170 instructions per warp and
+// 16 bytes per lane, and the scalar form took 172.
+typedef uint64_t f2;
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ f2 dup2(float x) { return pack2(x, x); }
+__device__ __forceinline__ float sum2(f2 a) {
+    float x, y;
+    unpack2(a, x, y);
+    return x + y;
+}
+
+// A lane's 16 bytes of a row: N elements as packed pairs, first the even ones
+// (0, 2), (4, 6), then the odd ones (1, 3), (5, 7), so that the interleaved
+// layout's partner of pair k is pair k ^ (N / 4) as a whole.
 template <typename T> struct Vec;
 template <> struct Vec<float> {
     static constexpr int N = 4;
-    static __device__ __forceinline__ void get(const uint4 &u, float (&x)[4]) {
-        x[0] = __uint_as_float(u.x);
-        x[1] = __uint_as_float(u.y);
-        x[2] = __uint_as_float(u.z);
-        x[3] = __uint_as_float(u.w);
+    static __device__ __forceinline__ void get(const uint4 &u, f2 (&x)[2]) {
+        x[0] = pack2(__uint_as_float(u.x), __uint_as_float(u.z));
+        x[1] = pack2(__uint_as_float(u.y), __uint_as_float(u.w));
     }
-    static __device__ __forceinline__ uint4 put(const float (&x)[4]) {
-        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    static __device__ __forceinline__ uint4 put(const f2 (&x)[2]) {
+        float a, b, c, d;
+        unpack2(x[0], a, c);
+        unpack2(x[1], b, d);
+        return make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(c), __float_as_uint(d));
     }
 };
 template <> struct Vec<__nv_bfloat16> {
     static constexpr int N = 8;
-    static __device__ __forceinline__ void get(const uint4 &u, float (&x)[8]) {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+    static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
+    static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+    static __device__ __forceinline__ void get(const uint4 &u, f2 (&x)[4]) {
+        x[0] = pack2(lo(u.x), lo(u.y));
+        x[1] = pack2(lo(u.z), lo(u.w));
+        x[2] = pack2(hi(u.x), hi(u.y));
+        x[3] = pack2(hi(u.z), hi(u.w));
     }
-    static __device__ __forceinline__ uint4 put(const float (&x)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            w[i] = *reinterpret_cast<uint32_t *>(&b);
-        }
-        return make_uint4(w[0], w[1], w[2], w[3]);
+    static __device__ __forceinline__ uint32_t two(float a, float b) {
+        __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<uint32_t *>(&v);
+    }
+    static __device__ __forceinline__ uint4 put(const f2 (&x)[4]) {
+        float e0, e1, e2, e3, o0, o1, o2, o3;
+        unpack2(x[0], e0, e1);
+        unpack2(x[1], e2, e3);
+        unpack2(x[2], o0, o1);
+        unpack2(x[3], o2, o3);
+        return make_uint4(two(e0, o0), two(e1, o1), two(e2, o2), two(e3, o3));
     }
 };
+// element of half h of packed pair k
+template <int V> __device__ __forceinline__ constexpr int elem(int k, int h) {
+    return k < V / 4 ? 2 * (2 * k + h) : 2 * (2 * (k - V / 4) + h) + 1;
+}
 
 template <int G> __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
     for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     return v;
+}
+template <int P> __device__ __forceinline__ float total2(const f2 (&x)[P]) {
+    f2 s = x[0];
+#pragma unroll
+    for (int k = 1; k < P; k++) s = fadd2(s, x[k]);
+    return sum2(s);
 }
 
 // V elements of a weight vector from element e.
@@ -82,12 +118,12 @@ __device__ __forceinline__ bool token_pos(const RopeArgs &r, long long at, int i
         if (r.axes == 1) {
             p[0] = index;
         } else if (r.axes == 2) {
-            p[0] = index / r.max[1];
+            p[0] = r.by1.div(index);
             p[1] = index - p[0] * r.max[1];
         } else {
-            const int ab = index / r.max[2];
+            const int ab = r.by2.div(index);
             p[2] = index - ab * r.max[2];
-            p[0] = ab / r.max[1];
+            p[0] = r.by1.div(ab);
             p[1] = ab - p[0] * r.max[1];
         }
         return true;
@@ -114,76 +150,103 @@ __device__ __forceinline__ bool token_pos(const RopeArgs &r, long long at, int i
 // interleaved, one per element when half.  e is the lane's first element.
 template <int V, bool HALF> struct Angles {
     static constexpr int N = HALF ? V : V / 2;
+    static constexpr uint32_t ALL = (1u << N) - 1u;
     float c[N], s[N];
     uint32_t on;  // bit i: pair i is rotated
     __device__ __forceinline__ void load(const RopeArgs &r, int e, bool rotated, const int (&p)[3]) {
         on = 0;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            c[i] = 1.f;
+            s[i] = 0.f;
+        }
+        if (!rotated) return;
+        // entry of pair q: the row of its axis plus q
+        uint32_t row[3];
+#pragma unroll
+        for (int a = 0; a < 3; a++) row[a] = r.off[a] + (uint32_t)p[a] * r.np[a] - r.first[a];
         const int first = HALF ? (e < r.pairs ? e : e - r.pairs) : e / 2;
 #pragma unroll
         for (int i = 0; i < N; i++) {
             const int q = first + i;
-            c[i] = 1.f;
-            s[i] = 0.f;
-            if (rotated && q < r.pairs) {
-                const int a = q < r.first[1] ? 0 : (q < r.first[2] ? 1 : 2);
-                const int pa = a == 0 ? p[0] : (a == 1 ? p[1] : p[2]);
-                const int fa = a == 0 ? 0 : (a == 1 ? r.first[1] : r.first[2]);
-                const int na = a == 0 ? r.np[0] : (a == 1 ? r.np[1] : r.np[2]);
-                const long long oa = a == 0 ? 0 : (a == 1 ? r.off[1] : r.off[2]);
-                const float2 t = __ldg(r.table + oa + (long long)pa * na + (q - fa));
+            if (q < r.pairs) {
+                const float2 t = __ldg(r.table + (q < r.first[1] ? row[0] : (q < r.first[2] ? row[1] : row[2])) + q);
                 c[i] = t.x;
                 s[i] = t.y;
                 on |= 1u << i;
             }
         }
     }
-    // x turned by the angles, or back (sign = -1).  All lanes of the warp call
-    // it; G lanes hold a row.  A pair that is not rotated keeps its elements
-    // (not x * 1 - y * 0: y may be infinite).
-    template <int G> __device__ __forceinline__ void turn(const RopeArgs &r, int e, float sign, float (&x)[V]) const {
-        if (HALF) {
-            // the partner element lies pairs / V lanes up (first half) or down
-            const int step = r.pairs / V;
-            const bool lower = e < r.pairs;
-            const int lane = threadIdx.x & 31;
-            const int src = lower ? lane + step : lane - step;
-            const float sg = lower ? -sign : sign;
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                const float y = __shfl_sync(0xffffffffu, x[i], src);
-                if (on >> i & 1u) x[i] = x[i] * c[i] + sg * s[i] * y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i++) {
-                const float a = x[2 * i], b = x[2 * i + 1], si = sign * s[i];
-                if (on >> i & 1u) {
-                    x[2 * i] = a * c[i] - b * si;
-                    x[2 * i + 1] = a * si + b * c[i];
-                }
-            }
-        }
+    // the lane that holds the partners of this lane's elements (half layout)
+    static __device__ __forceinline__ int partner(const RopeArgs &r, int e) {
+        const int lane = threadIdx.x & 31, step = r.pairs / V;
+        return e < r.pairs ? lane + step : lane - step;
     }
 };
 
-// x -> (x - mean) r in place; returns r.
-template <int V, int G> __device__ __forceinline__ float normalise(int norm, float eps, float (&x)[V]) {
-    constexpr float inv_d = 1.f / (V * G);
-    if (norm == NORM_LAYER) {
-        float s = 0.f;
+// Weight and bias folded into the rotation: turned_i = x_i ca_i + x'_i cb_i, with
+// x' the pair's other element, and rb the turned bias.  BACK: the inverse turn.
+template <int V, bool HALF> struct Coef {
+    static constexpr int P = V / 2;
+    f2 ca[P], cb[P], rb[P];
+    // w, b: weight and bias in the order of the lanes' packed pairs, P a lane
+    // (NULL: 1 and 0); lane: of the row's group.
+    template <bool BACK>
+    __device__ __forceinline__ void fold(const Angles<V, HALF> &g, const RopeArgs &r, int lane, const f2 *w,
+                                         const f2 *b) {
+        const int e = lane * V;
+        const bool lower = e < r.pairs;
+        // lanes at rest are their own partners
+        const int mate = HALF && e < 2 * r.pairs ? (lower ? lane + r.pairs / V : lane - r.pairs / V) : lane;
 #pragma unroll
-        for (int i = 0; i < V; i++) s += x[i];
-        const float mean = group_sum<G>(s) * inv_d;
-#pragma unroll
-        for (int i = 0; i < V; i++) x[i] -= mean;
+        for (int k = 0; k < P; k++) {
+            constexpr int d = HALF ? 1 : 2;
+            const int i0 = elem<V>(k, 0) / d, i1 = elem<V>(k, 1) / d;
+            const bool first = (HALF ? lower : k < V / 4) != BACK;
+            const f2 c = pack2(g.c[i0], g.c[i1]);
+            const f2 s = first ? pack2(-g.s[i0], -g.s[i1]) : pack2(g.s[i0], g.s[i1]);
+            const int o = HALF ? mate * P + k : lane * P + (k ^ (V / 4));
+            ca[k] = w ? mul2(w[lane * P + k], c) : c;
+            cb[k] = w ? mul2(w[o], s) : s;
+            rb[k] = b ? ffma2(b[o], s, mul2(b[lane * P + k], c)) : 0;
+        }
     }
-    float s = 0.f;
+    // All lanes of the warp call it; src: the lane of the partners (half layout).
+    // Pairs at rest (FULL: none) do not see their partner: it may be infinite.
+    template <bool FULL> __device__ __forceinline__ void turn(uint32_t on, int src, f2 (&x)[P]) const {
+        f2 y[P];
 #pragma unroll
-    for (int i = 0; i < V; i++) s += x[i] * x[i];
-    const float r = 1.f / sqrtf(group_sum<G>(s) * inv_d + eps);
+        for (int k = 0; k < P; k++) {
+            const f2 o = HALF ? __shfl_sync(0xffffffffu, x[k], src) : x[k ^ (V / 4)];
+            y[k] = mul2(x[k], ca[k]);
+            const f2 t = ffma2(o, cb[k], y[k]);
+            if (FULL) {
+                y[k] = t;
+            } else {
+                float y0, y1, t0, t1;
+                unpack2(y[k], y0, y1);
+                unpack2(t, t0, t1);
+                constexpr int d = HALF ? 1 : 2;
+                y[k] = pack2(on >> (elem<V>(k, 0) / d) & 1u ? t0 : y0, on >> (elem<V>(k, 1) / d) & 1u ? t1 : y1);
+            }
+        }
 #pragma unroll
-    for (int i = 0; i < V; i++) x[i] *= r;
-    return r;
+        for (int k = 0; k < P; k++) x[k] = y[k];
+    }
+};
+
+// LAYER: x - mean in place.  Returns r = 1 / sqrt(mean square + eps).
+template <int P, int G> __device__ __forceinline__ float centre(int norm, float eps, f2 (&x)[P]) {
+    constexpr float inv_d = 1.f / (2 * P * G);
+    if (norm == NORM_LAYER) {
+        const f2 m = dup2(group_sum<G>(total2(x)) * -inv_d);
+#pragma unroll
+        for (int k = 0; k < P; k++) x[k] = fadd2(x[k], m);
+    }
+    f2 s = mul2(x[0], x[0]);
+#pragma unroll
+    for (int k = 1; k < P; k++) s = ffma2(x[k], x[k], s);
+    return rsqrtf(group_sum<G>(sum2(s)) * inv_d + eps);
 }
 
 // The sequence of a stacked row (binary search over q_start, every index within
@@ -203,167 +266,340 @@ __device__ __forceinline__ bool find_seq(const PageArgs &g, int row, int &seq, i
     return row >= a && row < b;
 }
 
-template <typename T, int D, bool HALF, int HC>
-__global__ void __launch_bounds__(NT) norm_rope_kernel(const __grid_constant__ RowArgs a) {
-    constexpr int V = Vec<T>::N, G = D / V, TOK = NT / G;
-    // chunk = HC heads of one of the tensors
-    int chunk = blockIdx.x, ti = 0;
-    int total = 0;
-#pragma unroll
-    for (int i = 0; i < 3; i++)
-        if (i < a.nt) total += (a.t[i].heads + HC - 1) / HC;
-    const long long tile = chunk / total;
-    chunk -= (int)tile * total;
-    while (chunk >= (a.t[ti].heads + HC - 1) / HC) chunk -= (a.t[ti++].heads + HC - 1) / HC;
-    const RowTensor &t = a.t[ti];
-    const int h0 = chunk * HC, nh = min(HC, t.heads - h0);
-    const int e = (threadIdx.x % G) * V;
-    const long long tok = tile * TOK + threadIdx.x / G;
-    bool live = tok < (long long)a.batch * a.n;
-    const int b = live ? (int)(tok / a.n) : 0;
-    const int i = live ? (int)(tok - (long long)b * a.n) : 0;
-
-    int index = i;
-    long long base = b * t.y.sb + i * t.y.sn;  // first element of the token's output rows
-    bool store = live;
-    if (a.page.seqs) {
-        int seq = 0, place = 0;
-        live = live && find_seq(a.page, i, seq, place);
-        store = live;
-        index = place;
-        if (live && (place < 0 || (place >> a.page.page_log2) >= a.page.max_pages)) {
-            set_status(a.status, ST_INVALID);
-            store = !t.paged;
-            index = place < 0 ? 0 : place;
-        } else if (live && t.paged) {
-            const int page = __ldg(a.page.block_table + (long long)seq * a.page.max_pages + (place >> a.page.page_log2));
-            if (page < 0 || page >= a.page.num_pages) {
-                set_status(a.status, ST_INVALID);
-                store = false;
-            } else {
-                base = (((long long)page * a.page.kv_heads) << a.page.page_log2) * D +
-                       (long long)(place & ((1 << a.page.page_log2) - 1)) * D;
-            }
-        }
-    }
-    const T *x = (const T *)t.x.p + b * t.x.sb + i * t.x.sn + h0 * t.x.sh + e;
-    T *y = (T *)t.y.p + base + h0 * t.y.sh + e;
-    uint4 u[HC];
-#pragma unroll
-    for (int h = 0; h < HC; h++) {
-        u[h] = make_uint4(0u, 0u, 0u, 0u);
-        if (live && h < nh) u[h] = __ldg((const uint4 *)(x + h * t.x.sh));
-    }
-    if (!t.copy) {
-        int p[3];
-        const bool rotated = live && token_pos(a.rope, b * a.rope.pos_batch + (long long)i * a.rope.axes, index, p, a.status);
-        Angles<V, HALF> ang;
-        ang.load(a.rope, e, rotated, p);
-        float w[V], bias[V];
-        if (a.norm != NORM_NONE) {
-            load_w<V>(t.w, a.w_f32, e, 1.f, w);
-            load_w<V>(t.b, a.w_f32, e, 0.f, bias);
-        }
-#pragma unroll
-        for (int h = 0; h < HC; h++) {
-            float v[V];
-            Vec<T>::get(u[h], v);
-            if (a.norm != NORM_NONE) {
-                normalise<V, G>(a.norm, a.eps, v);
-#pragma unroll
-                for (int k = 0; k < V; k++) v[k] = v[k] * w[k] + bias[k];
-            }
-            if (a.rope.axes) ang.template turn<G>(a.rope, e, 1.f, v);
-            u[h] = Vec<T>::put(v);
-        }
-    }
-#pragma unroll
-    for (int h = 0; h < HC; h++)
-        if (store && h < nh) *(uint4 *)(y + h * t.y.sh) = u[h];
+// 16 bytes to shared memory, zeros where !ok (nothing is read then)
+__device__ __forceinline__ void copy16(uint4 *dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
 }
 
-// Gradients.  A group takes HC heads of one token at a time, like the forward
-// kernel, and the CTA walks its share of (token tile, head chunk) items, so
-// that each lane sums its elements' dw and db over all of them in registers;
-// the CTA's sums go to part[cta] and back_sum_kernel adds the CTAs in order.
-template <typename T, int D, bool HALF, int HC>
-__global__ void __launch_bounds__(NT) norm_rope_back_kernel(const __grid_constant__ BackArgs a) {
-    constexpr int V = Vec<T>::N, G = D / V, TOK = NT / G;
-    __shared__ float red[2][TOK][D];
+// Norm and rotation.  The CTA's groups are TT tokens x HS heads; a unit is HS x HC
+// heads of one tensor, an item `per` units of one tile of TT tokens.  So a CTA
+// reads HS x HC neighbouring heads of a token at a time (2 KB at d = 128), which
+// DRAM needs: one head of many tokens at a time ran at 5.4 instead of 6.2 TB/s.
+// And a group folds its coefficients once per token and tensor.  CTAs take items
+// in turn, so that those at work at one time share DRAM pages.  A lane's own 16
+// bytes of each row come through a ring of STEPS steps of cp.async copies: loads
+// are in flight all the time with few registers.
+template <typename T, int D, bool HALF, bool STAT, int HC>
+__global__ void __launch_bounds__(NT, FWD_CTAS) norm_rope_kernel(const __grid_constant__ RowArgs a, int parts, int per, const FastDiv by_parts) {
+    constexpr int V = Vec<T>::N, P = V / 2, G = D / V, STEPS = FWD_STEPS, UH = HS * HC, TT = NT / G / HS;
+    extern __shared__ __align__(16) uint4 ring_raw[];
+    uint4(*ring)[HC][NT] = reinterpret_cast<uint4(*)[HC][NT]>(ring_raw);
+    // weights and biases of q and k in the order of the lanes' packed pairs
+    __shared__ f2 sw[2][2][STAT ? D / 2 : 1];
+    const int lane = threadIdx.x % G, grp = threadIdx.x / G / HS, hs = threadIdx.x / G % HS, e = lane * V;
+    const int tokens = a.batch * a.n;
+    int units[3], all = 0;
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        units[i] = i < a.nt ? (a.t[i].heads + UH - 1) / UH : 0;
+        all += units[i];
+    }
+    const int items = ((tokens + TT - 1) / TT) * parts;  // the host checks the range
+    const int src = Angles<V, HALF>::partner(a.rope, e);
+
+    // The units of one tensor from unit u of item `it` on.  Lanes past the last
+    // token walk them too and store nothing.
+    struct Run {
+        int ti, tok, b, i, h0, h1, next;  // next: the unit behind, 0 = the item ends
+    };
+    auto run_of = [&](int it, int u) {
+        Run m;
+        const int tile = by_parts.div(it), u0 = (it - tile * parts) * per, u1 = min(u0 + per, all);
+        int first = u0 + u;
+        m.ti = first < units[0] ? 0 : (first < units[0] + units[1] ? 1 : 2);
+        const int base = m.ti == 0 ? 0 : (m.ti == 1 ? units[0] : units[0] + units[1]);
+        const int last = min(u1, base + (m.ti == 0 ? units[0] : (m.ti == 1 ? units[1] : units[2])));
+        m.next = last < u1 ? last - u0 : 0;
+        m.tok = tile * TT + grp;
+        const int tok = min(m.tok, tokens - 1);
+        m.b = a.batch > 1 ? a.by_n.div(tok) : 0;
+        m.i = tok - m.b * a.n;
+        m.h0 = (first - base) * UH;
+        m.h1 = min((last - base) * UH, a.t[m.ti].heads);
+        return m;
+    };
+
+    // the loading side, STEPS - 1 steps ahead of the computing side
+    int lit = blockIdx.x, lu = 0, lh = 0, lh1 = 0, slot = 0;
+    const T *lx = nullptr;
+    long long lsh = 0;
+    auto enter = [&]() {
+        if (lit >= items) return;
+        const Run m = run_of(lit, lu);
+        const View &x = a.t[m.ti].x;
+        lu = m.next;
+        lh = m.h0;
+        lh1 = m.h1;
+        lsh = HS * x.sh;
+        lx = (const T *)x.p + m.b * x.sb + m.i * x.sn + (m.h0 + hs) * x.sh + e;
+    };
+    auto load_step = [&]() {
+        if (lit < items) {
+#pragma unroll
+            for (int j = 0; j < HC; j++) {
+                copy16(&ring[slot][j][threadIdx.x], lx, lh + j * HS + hs < lh1);
+                lx += lsh;
+            }
+            lh += UH;
+            if (lh >= lh1) {
+                if (lu == 0) lit += gridDim.x;
+                enter();
+            }
+        }
+        slot = slot == STEPS - 1 ? 0 : slot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    enter();
+#pragma unroll
+    for (int i = 0; i < STEPS - 1; i++) load_step();
+
+    if (STAT) {
+        for (int i = threadIdx.x; i < 2 * D; i += NT) {
+            const int ti = i / D, which = i / (D / 2) & 1, c = i % (D / 2);
+            if (ti >= a.nt || a.t[ti].copy) continue;
+            const void *p = which ? a.t[ti].b : a.t[ti].w;
+            float v[2] = {which ? 0.f : 1.f, which ? 0.f : 1.f};
+            if (p) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const int x = c / P * V + elem<V>(c % P, h);
+                    v[h] = a.w_f32 ? ((const float *)p)[x] : __bfloat162float(((const __nv_bfloat16 *)p)[x]);
+                }
+            }
+            sw[ti][which][c] = pack2(v[0], v[1]);
+        }
+        __syncthreads();
+    }
+    int at = 0, u = 0;
+    for (int it = blockIdx.x; it < items;) {
+        const Run m = run_of(it, u);
+        const RowTensor &t = a.t[m.ti];
+        u = m.next;
+        if (u == 0) it += gridDim.x;
+        bool live = m.tok < tokens;
+        int index = m.i;
+        long long at_y = m.b * t.y.sb + m.i * t.y.sn;
+        bool store = live;
+        if (a.page.seqs) {
+            int seq = 0, place = 0;
+            live = find_seq(a.page, m.i, seq, place) && live;
+            store = live;
+            index = max(place, 0);
+            if (live) {
+                int page = -1;
+                if (place >= 0 && (place >> a.page.page_log2) < a.page.max_pages)
+                    page = __ldg(a.page.block_table + (long long)seq * a.page.max_pages + (place >> a.page.page_log2));
+                const bool fits = page >= 0 && page < a.page.num_pages;
+                if (!fits) set_status(a.status, ST_INVALID);
+                if (t.paged) {
+                    store = fits;
+                    at_y = ((((long long)page * a.page.kv_heads) << a.page.page_log2) +
+                            (place & ((1 << a.page.page_log2) - 1))) * D;
+                }
+            }
+        }
+        Coef<V, HALF> k;
+        uint32_t on = 0;
+        if (!t.copy) {
+            int p[3];
+            Angles<V, HALF> ang;
+            const bool rotated =
+                live && token_pos(a.rope, m.b * a.rope.pos_batch + (long long)m.i * a.rope.axes, index, p, a.status);
+            ang.load(a.rope, e, rotated, p);
+            on = ang.on;
+            k.template fold<false>(ang, a.rope, lane, STAT && t.w ? sw[m.ti][0] : nullptr, STAT && t.b ? sw[m.ti][1] : nullptr);
+        }
+        T *y = (T *)t.y.p + at_y + (m.h0 + hs) * t.y.sh + e;
+        const bool full = __all_sync(0xffffffffu, on == Angles<V, HALF>::ALL);
+        for (int h = m.h0; h < m.h1; h += UH) {
+            load_step();
+            asm volatile("cp.async.wait_group %0;" ::"n"(STEPS - 1) : "memory");
+#pragma unroll
+            for (int j = 0; j < HC; j++) {
+                if (h + j * HS >= m.h1) break;
+                uint4 row = ring[at][j][threadIdx.x];
+                if (!t.copy) {
+                    f2 v[P];
+                    Vec<T>::get(row, v);
+                    f2 r = 0;
+                    if (STAT) r = dup2(centre<P, G>(a.norm, a.eps, v));
+                    if (full)
+                        k.template turn<true>(on, src, v);
+                    else
+                        k.template turn<false>(on, src, v);
+                    if (STAT) {
+#pragma unroll
+                        for (int i = 0; i < P; i++) v[i] = ffma2(v[i], r, k.rb[i]);
+                    }
+                    row = Vec<T>::put(v);
+                }
+                if (store && h + j * HS + hs < m.h1) *(uint4 *)y = row;
+                y += HS * t.y.sh;
+            }
+            at = at == STEPS - 1 ? 0 : at + 1;
+        }
+    }
+}
+
+// Gradients.  With n = r x (x centred): e = g' w, c = r^3 mean(e x),
+//   dx = r (e - [mean e]) - c x,  dw += (g' x) r,  db += g',
+// both means in one round of shuffles.  The CTAs take items (token tile,
+// run of heads) in turn, in steps of HC heads; a lane's own
+// g and x come through a ring of STEPS steps of cp.async copies, two steps ahead
+// (64 bytes a step and thread: the registers alone held too few loads in flight,
+// 39% of the memory's rate).  Each lane sums its elements' dw and db over all its
+// rows in registers; the CTA's sums go to part[cta] and back_sum_kernel adds the
+// CTAs in order.
+template <typename T, int D, bool HALF, bool STAT>
+__global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __grid_constant__ BackArgs a) {
+    constexpr int V = Vec<T>::N, P = V / 2, G = D / V, TOK = NT / G, TT = TOK / HS, HC = BACK_HC, UH = HS * HC, STEPS = BACK_STEPS;
+    constexpr int PER = STAT ? 2 * HC : HC;  // pieces of 16 bytes a step
+    extern __shared__ __align__(16) uint4 ring_raw[];
+    uint4(*ring)[PER][NT] = reinterpret_cast<uint4(*)[PER][NT]>(ring_raw);
+    static_assert(!STAT || STEPS * PER * NT * 16 >= 2 * TOK * D * (int)sizeof(float), "the sums reuse the ring");
     const int ti = (int)blockIdx.x < a.ctas[0] ? 0 : 1;
     const int cta = blockIdx.x - (ti ? a.ctas[0] : 0);
     const BackTensor &t = a.t[ti];
-    const int grp = threadIdx.x / G, e = (threadIdx.x % G) * V;
-    const long long tokens = (long long)a.batch * a.n;
-    const int chunks = (t.heads + HC - 1) / HC;
-    const long long items = (tokens + TOK - 1) / TOK * chunks;
-    float w[V], dw[V], db[V];
-    load_w<V>(t.w, a.w_f32, e, 1.f, w);
+    const int grp = threadIdx.x / G, hs = grp % HS, e = (threadIdx.x % G) * V;
+    const int tokens = a.batch * a.n;
+    // an item: a.run heads of one tile of TT tokens; the CTAs take them in turn
+    const int runs = (t.heads + a.run - 1) / a.run;
+    const int items = ((tokens + TT - 1) / TT) * runs;  // the host checks the range
+    const int src = Angles<V, HALF>::partner(a.rope, e);
+
+    // Lanes past the last token walk its items too and store nothing.
+    struct Item {
+        int tok, b, i, h0, h1;
+    };
+    auto item_of = [&](int it) {
+        Item m;
+        const int tile = a.by_runs[ti].div(it);
+        m.tok = tile * TT + grp / HS;
+        const int tok = min(m.tok, tokens - 1);
+        m.b = a.batch > 1 ? a.by_n.div(tok) : 0;
+        m.i = tok - m.b * a.n;
+        m.h0 = (it - tile * runs) * a.run;
+        m.h1 = min(m.h0 + a.run, t.heads);
+        return m;
+    };
+
+    // the loading side: steps of all items in order, ahead of the computing side
+    int lit = cta, lh = 0, lh1 = 0, slot = 0;
+    bool llive = false;
+    const T *lg = nullptr, *lx = nullptr;
+    auto enter = [&]() {
+        if (lit >= items) return;
+        const Item m = item_of(lit);
+        lh = m.h0;
+        lh1 = m.h1;
+        llive = m.tok < tokens;
+        lg = (const T *)t.g.p + m.b * t.g.sb + m.i * t.g.sn + (m.h0 + hs) * t.g.sh + e;
+        lx = (const T *)t.x.p + m.b * t.x.sb + m.i * t.x.sn + (m.h0 + hs) * t.x.sh + e;
+    };
+    auto load_step = [&]() {
+        if (lit < items) {
 #pragma unroll
-    for (int k = 0; k < V; k++) dw[k] = db[k] = 0.f;
-    for (long long it = cta; it < items; it += a.ctas[ti]) {
-        const long long tile = it / chunks;
-        const int h0 = (int)(it - tile * chunks) * HC, nh = min(HC, t.heads - h0);
-        const long long tok = tile * TOK + grp;
-        const bool live = tok < tokens;
-        const int b = live ? (int)(tok / a.n) : 0;
-        const int i = live ? (int)(tok - (long long)b * a.n) : 0;
-        const T *g = (const T *)t.g.p + b * t.g.sb + i * t.g.sn + h0 * t.g.sh + e;
-        const T *x = (const T *)t.x.p + b * t.x.sb + i * t.x.sn + h0 * t.x.sh + e;
-        T *dx = (T *)t.dx.p + b * t.dx.sb + i * t.dx.sn + h0 * t.dx.sh + e;
-        uint4 ug[HC], ux[HC];
-#pragma unroll
-        for (int h = 0; h < HC; h++) {
-            ug[h] = ux[h] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && h < nh) {
-                ug[h] = __ldg((const uint4 *)(g + h * t.g.sh));
-                if (a.norm != NORM_NONE) ux[h] = __ldg((const uint4 *)(x + h * t.x.sh));
+            for (int j = 0; j < HC; j++) {
+                const bool ok = llive && lh + j * HS + hs < lh1;
+                copy16(&ring[slot][j][threadIdx.x], lg, ok);
+                if (STAT) copy16(&ring[slot][(HC + j) % PER][threadIdx.x], lx, ok);
+                lg += HS * t.g.sh;
+                lx += HS * t.x.sh;
+            }
+            lh += UH;
+            if (lh >= lh1) {
+                lit += a.ctas[ti];
+                enter();
             }
         }
-        int p[3];
-        const bool rotated = live && token_pos(a.rope, b * a.rope.pos_batch + (long long)i * a.rope.axes, i, p, a.status);
-        Angles<V, HALF> ang;
-        ang.load(a.rope, e, rotated, p);
+        slot = slot == STEPS - 1 ? 0 : slot + 1;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    enter();
 #pragma unroll
-        for (int h = 0; h < HC; h++) {
-            float gv[V];
-            Vec<T>::get(ug[h], gv);
-            if (a.rope.axes) ang.template turn<G>(a.rope, e, -1.f, gv);
-            if (a.norm != NORM_NONE) {
-                float xv[V];
-                Vec<T>::get(ux[h], xv);
-                const float r = normalise<V, G>(a.norm, a.eps, xv);
-                float m1 = 0.f, m2 = 0.f;
-                const bool in = live && h < nh;
+    for (int i = 0; i < STEPS - 1; i++) load_step();
+
+    f2 w[P], dw[P], db[P];
+    if (STAT) {
+        float wv[V];
+        load_w<V>(t.w, a.w_f32, e, 1.f, wv);
 #pragma unroll
-                for (int k = 0; k < V; k++) {
-                    if (in) {
-                        dw[k] += gv[k] * xv[k];
-                        db[k] += gv[k];
-                    }
-                    gv[k] *= w[k];
-                    m1 += gv[k];
-                    m2 += gv[k] * xv[k];
-                }
-                m2 = group_sum<G>(m2) * (1.f / D);
-                m1 = a.norm == NORM_LAYER ? group_sum<G>(m1) * (1.f / D) : 0.f;
-#pragma unroll
-                for (int k = 0; k < V; k++) gv[k] = r * (gv[k] - m1 - xv[k] * m2);
-            }
-            if (live && h < nh) *(uint4 *)(dx + h * t.dx.sh) = Vec<T>::put(gv);
+        for (int k = 0; k < P; k++) {
+            w[k] = pack2(wv[elem<V>(k, 0)], wv[elem<V>(k, 1)]);
+            dw[k] = db[k] = 0;
         }
     }
-    if (!a.part) return;
+    int at = 0;
+    for (int it = cta; it < items; it += a.ctas[ti]) {
+        const Item m = item_of(it);
+        const bool live = m.tok < tokens;
+        T *dx = (T *)t.dx.p + m.b * t.dx.sb + m.i * t.dx.sn + (m.h0 + hs) * t.dx.sh + e;
+        Coef<V, HALF> turn;
+        uint32_t on;
+        {
+            int p[3];
+            Angles<V, HALF> ang;
+            const bool rotated =
+                token_pos(a.rope, m.b * a.rope.pos_batch + (long long)m.i * a.rope.axes, m.i, p, a.status);
+            ang.load(a.rope, e, rotated, p);
+            on = ang.on;
+            turn.template fold<true>(ang, a.rope, e / V, nullptr, nullptr);
+        }
+        for (int h = m.h0; h < m.h1; h += UH) {
+            load_step();
+            asm volatile("cp.async.wait_group %0;" ::"n"(STEPS - 1) : "memory");
 #pragma unroll
-    for (int k = 0; k < V; k++) {
-        red[0][grp][e + k] = dw[k];
-        red[1][grp][e + k] = db[k];
+            for (int j = 0; j < HC; j++) {
+                if (h + j * HS >= m.h1) break;
+                const bool in = live && h + j * HS + hs < m.h1;  // else g and x are zeros
+                f2 g[P];
+                Vec<T>::get(ring[at][j][threadIdx.x], g);
+                turn.template turn<false>(on, src, g);
+                if (STAT) {
+                    f2 x[P], s1 = 0, s2 = 0;
+                    Vec<T>::get(ring[at][(HC + j) % PER][threadIdx.x], x);
+                    const float r = centre<P, G>(a.norm, a.eps, x);
+                    const f2 rs = dup2(in ? r : 0.f);
+#pragma unroll
+                    for (int k = 0; k < P; k++) {
+                        const f2 p = mul2(g[k], x[k]);
+                        dw[k] = ffma2(p, rs, dw[k]);
+                        db[k] = fadd2(db[k], g[k]);
+                        s2 = ffma2(p, w[k], s2);
+                        g[k] = mul2(g[k], w[k]);
+                        s1 = fadd2(s1, g[k]);
+                    }
+                    const f2 c = dup2(group_sum<G>(sum2(s2)) * (-1.f / D) * r * r * r);
+                    const f2 m1 = dup2(a.norm == NORM_LAYER ? group_sum<G>(sum2(s1)) * (-1.f / D) * r : 0.f);
+                    const f2 r2 = dup2(r);
+#pragma unroll
+                    for (int k = 0; k < P; k++) g[k] = ffma2(g[k], r2, ffma2(x[k], c, m1));
+                }
+                if (in) *(uint4 *)dx = Vec<T>::put(g);
+                dx += HS * t.dx.sh;
+            }
+            at = at == STEPS - 1 ? 0 : at + 1;
+        }
+    }
+    if (!STAT || !a.part) return;
+    __syncthreads();  // every lane is through with its ring
+    float *red = reinterpret_cast<float *>(ring);  // [2][TOK][D]
+#pragma unroll
+    for (int k = 0; k < P; k++) {
+        float x, y;
+        unpack2(dw[k], x, y);
+        red[grp * D + e + elem<V>(k, 0)] = x;
+        red[grp * D + e + elem<V>(k, 1)] = y;
+        unpack2(db[k], x, y);
+        red[(TOK + grp) * D + e + elem<V>(k, 0)] = x;
+        red[(TOK + grp) * D + e + elem<V>(k, 1)] = y;
     }
     __syncthreads();
     for (int c = threadIdx.x; c < 2 * D; c += NT) {
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < TOK; k++) s += red[c / D][k][c % D];
+        for (int k = 0; k < TOK; k++) s += red[((c / D) * TOK + k) * D + c % D];
         a.part[(size_t)blockIdx.x * 2 * D + c] = s;
     }
 }
@@ -403,37 +639,60 @@ __global__ void rope_table_kernel(const __grid_constant__ RopeArgs r, const __gr
     table[i] = make_float2((float)(c * f.mag), (float)(s * f.mag));
 }
 
-template <typename T, int D, bool HALF, int HC> int launch_rows(const RowArgs &a, cudaStream_t st) {
-    constexpr int TOK = NT / (D / Vec<T>::N);
-    long long chunks = 0;
-    for (int i = 0; i < a.nt; i++) chunks += (a.t[i].heads + HC - 1) / HC;
-    const long long grid = ((long long)a.batch * a.n + TOK - 1) / TOK * chunks;
-    if (grid > 0x7fffffffLL) return -1;
-    norm_rope_kernel<T, D, HALF, HC><<<(unsigned)grid, NT, 0, st>>>(a);
+typedef void (*FwdKernel)(const RowArgs, int, int, const FastDiv);
+template <typename T, int D, int HC> FwdKernel fwd_kernel(bool half, bool stat) {
+    if (stat) return half ? norm_rope_kernel<T, D, true, true, HC> : norm_rope_kernel<T, D, false, true, HC>;
+    return half ? norm_rope_kernel<T, D, true, false, HC> : norm_rope_kernel<T, D, false, false, HC>;
+}
+constexpr int fwd_smem(int HC) { return FWD_STEPS * HC * NT * 16; }
+
+template <typename T, int D, int HC> int launch_rows(const RowArgs &a, int num_sms, cudaStream_t st) {
+    constexpr int TT = NT / (D / Vec<T>::N) / HS, UH = HS * HC;
+    long long units = 0;
+    for (int i = 0; i < a.nt; i++) units += (a.t[i].heads + UH - 1) / UH;
+    const long long items = ((long long)a.batch * a.n + TT - 1) / TT * units, ctas = (long long)FWD_CTAS * num_sms;
+    if (items > 0x3fffffffLL) return -1;
+    // as many rounds as the items need, and only as many CTAs as fill the rounds
+    const long long rounds = (items + ctas - 1) / ctas;
+    fwd_kernel<T, D, HC>(a.rope.half, a.norm != NORM_NONE)<<<(unsigned)((items + rounds - 1) / rounds), NT, fwd_smem(HC), st>>>(
+        a, (int)units, 1, FastDiv((uint32_t)units));
     note_launch();
     return 0;
 }
-// HC = 1 where HC = 8 would leave SMs without a CTA (few tokens): more groups
-// at work on the same rows.
+// HC = 1 where units of 8 heads would leave SMs without a CTA (few tokens)
 template <typename T, int D> int launch_rows_d(const RowArgs &a, int num_sms, cudaStream_t st) {
-    constexpr int TOK = NT / (D / Vec<T>::N);
-    long long chunks = 0;
-    for (int i = 0; i < a.nt; i++) chunks += (a.t[i].heads + 7) / 8;
-    const bool many = ((long long)a.batch * a.n + TOK - 1) / TOK * chunks >= 2 * num_sms;
-    if (a.rope.half) return many ? launch_rows<T, D, true, 8>(a, st) : launch_rows<T, D, true, 1>(a, st);
-    return many ? launch_rows<T, D, false, 8>(a, st) : launch_rows<T, D, false, 1>(a, st);
+    constexpr int TT = NT / (D / Vec<T>::N) / HS;
+    long long units = 0;
+    for (int i = 0; i < a.nt; i++) units += (a.t[i].heads + 7) / 8;
+    const bool many = ((long long)a.batch * a.n + TT - 1) / TT * units >= num_sms;
+    return many ? launch_rows<T, D, FWD_HC>(a, num_sms, st) : launch_rows<T, D, 1>(a, num_sms, st);
 }
 
-template <typename T, int D> void launch_back(const BackArgs &a, cudaStream_t st) {
-    const int grid = a.ctas[0] + a.ctas[1];
-    if (a.rope.half)
-        norm_rope_back_kernel<T, D, true, 2><<<grid, NT, 0, st>>>(a);
-    else
-        norm_rope_back_kernel<T, D, false, 2><<<grid, NT, 0, st>>>(a);
-    note_launch();
+typedef void (*BackKernel)(const BackArgs);
+template <typename T, int D> BackKernel back_kernel(bool half, bool stat) {
+    if (stat) return half ? norm_rope_back_kernel<T, D, true, true> : norm_rope_back_kernel<T, D, false, true>;
+    return half ? norm_rope_back_kernel<T, D, true, false> : norm_rope_back_kernel<T, D, false, false>;
 }
+constexpr int back_smem(bool stat) { return BACK_STEPS * (stat ? 2 : 1) * BACK_HC * NT * 16; }
 
 }  // namespace
+
+namespace {
+template <typename T, int D> int setup(int half, bool stat) {
+    auto raise = [](const void *fn, int smem) {
+        return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
+    };
+    return raise((const void *)fwd_kernel<T, D, FWD_HC>(half, stat), fwd_smem(FWD_HC)) &&
+                   raise((const void *)back_kernel<T, D>(half, stat), back_smem(stat))
+               ? 0
+               : -1;
+}
+}  // namespace
+int rope_setup(int dtype, int D, int half, int norm) {
+    const bool stat = norm != NORM_NONE;
+    if (dtype == DT_BF16) return D == 64 ? setup<__nv_bfloat16, 64>(half, stat) : setup<__nv_bfloat16, 128>(half, stat);
+    return D == 64 ? setup<float, 64>(half, stat) : setup<float, 128>(half, stat);
+}
 
 void k_rope_table(const RopeArgs &r, const FreqArgs &f, float2 *table, cudaStream_t st) {
     const long long total = r.off[r.axes - 1] + (long long)r.max[r.axes - 1] * r.np[r.axes - 1];
@@ -448,20 +707,34 @@ int k_norm_rope(const RowArgs &a, int dtype, int D, int num_sms, cudaStream_t st
     return D == 64 ? launch_rows_d<float, 64>(a, num_sms, st) : launch_rows_d<float, 128>(a, num_sms, st);
 }
 
-int back_ctas(int num_sms) { return 2 * num_sms + 2; }
+int back_ctas(int num_sms) { return BACK_CTAS * num_sms + 2; }
 
 int k_norm_rope_back(BackArgs &a, int dtype, int D, int num_sms, cudaStream_t st) {
     // the tensors' CTAs in proportion to their heads
-    const int total = 2 * num_sms, h0 = a.t[0].heads, h1 = a.t[1].heads;
+    const int total = BACK_CTAS * num_sms, h0 = a.t[0].heads, h1 = a.t[1].heads;
     a.ctas[0] = h0 ? max(1, (int)((long long)total * h0 / (h0 + h1))) : 0;
     a.ctas[1] = h1 ? max(1, total - a.ctas[0]) : 0;
-    if (dtype == DT_BF16) {
-        if (D == 64) launch_back<__nv_bfloat16, 64>(a, st);
-        else launch_back<__nv_bfloat16, 128>(a, st);
-    } else {
-        if (D == 64) launch_back<float, 64>(a, st);
-        else launch_back<float, 128>(a, st);
+    const long long tt = NT / (D / (dtype == DT_BF16 ? 8 : 4)) / HS, tiles = ((long long)a.batch * a.n + tt - 1) / tt;
+    a.run = BACK_MOST;
+    // few tokens: shorter runs, more CTAs at work
+    if (tiles * ((max(h0, h1) + a.run - 1) / a.run) < total) a.run = BACK_HC * HS;
+    for (int i = 0; i < 2; i++) {
+        const int heads = a.t[i].heads;
+        if (!heads) continue;
+        const long long runs = (heads + a.run - 1) / a.run, items = tiles * runs;
+        if (items > 0x3fffffffLL) return -1;
+        a.by_runs[i] = FastDiv((uint32_t)runs);
+        // as many rounds as the items need, and only as many CTAs as fill the rounds
+        const long long rounds = (items + a.ctas[i] - 1) / a.ctas[i];
+        a.ctas[i] = (int)((items + rounds - 1) / rounds);
     }
+    const bool stat = a.norm != NORM_NONE;
+    BackKernel fn = dtype == DT_BF16 ? (D == 64 ? back_kernel<__nv_bfloat16, 64>(a.rope.half, stat)
+                                                : back_kernel<__nv_bfloat16, 128>(a.rope.half, stat))
+                                     : (D == 64 ? back_kernel<float, 64>(a.rope.half, stat)
+                                                : back_kernel<float, 128>(a.rope.half, stat));
+    fn<<<a.ctas[0] + a.ctas[1], NT, back_smem(stat), st>>>(a);
+    note_launch();
     if (a.part) {
         back_sum_kernel<<<4, 1024, 0, st>>>(a, D);
         note_launch();

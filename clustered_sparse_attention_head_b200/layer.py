@@ -86,8 +86,14 @@ class AttnLayer:
         with torch.cuda.device(self.device):
             check("ac_layer_create", self.lib.ac_layer_create(byref(c), byref(self._layer)))
         self.heads, self.kv_heads, self.d, self.axes = c.heads, c.kv_heads, c.d, c.rope_axes
+        self.normed = c.norm != _abi.AC_NORM_NONE
         self.dtype, self.w_dtype = _DTYPES[cfg.dtype][1], _DTYPES[cfg.w_dtype][1]
+        self._index = self.device.index
         nb = ctypes.c_size_t()
+        self._pairs = 0
+        if self.axes:
+            check("ac_rope_table_size", self.lib.ac_rope_table_size(self._layer, byref(nb)))
+            self._pairs = nb.value // 8
         check("ac_layer_workspace_size", self.lib.ac_layer_workspace_size(self._layer, byref(nb)))
         self.ws_bytes = nb.value
         if workspace is None:
@@ -96,6 +102,7 @@ class AttnLayer:
             raise ValueError("AttnLayer: workspace must be a contiguous tensor on the layer's device")
         self.ws = workspace
         self._ws_have = workspace.numel() * workspace.element_size()
+        self._ws_ptr = workspace.data_ptr()
 
     def close(self):
         if self._layer:
@@ -109,37 +116,54 @@ class AttnLayer:
             pass
 
     # --------------------------------------------------------------- helpers
-    def _view(self, t, name, lead, heads):
-        """ac_tensor of a [*lead, heads, d] view; lead is (batch, tokens) or (tokens,)."""
-        if t.dtype != self.dtype or t.device != self.device:
-            raise ValueError(f"{name}: {t.dtype} on {t.device}, expected {self.dtype} on {self.device}")
-        if tuple(t.shape) != (*lead, heads, self.d):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(*lead, heads, self.d)}")
-        s = t.stride()
-        if s[-1] != 1:
+    # The calls are a few microseconds on the GPU for few tokens, so these keep
+    # to the cheapest forms that check everything.
+    def _rows(self, t, name, tokens, heads):
+        """ac_tensor of a [tokens, heads, d] view."""
+        if t.dtype != self.dtype or t.device != self.device or t.shape != (tokens, heads, self.d):
+            self._refuse(t, name, (tokens, heads, self.d))
+        sn, sh, one = t.stride()
+        if one != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        return _abi.ac_tensor(t.data_ptr(), s[0] if len(s) == 4 else 0, s[-3], s[-2])
+        return byref(_abi.ac_tensor(t.data_ptr(), 0, sn, sh))
+
+    def _bnhd(self, t, name, batch, n, heads):
+        """ac_tensor of a [batch, n, heads, d] view."""
+        if t.dtype != self.dtype or t.device != self.device or t.shape != (batch, n, heads, self.d):
+            self._refuse(t, name, (batch, n, heads, self.d))
+        sb, sn, sh, one = t.stride()
+        if one != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        return byref(_abi.ac_tensor(t.data_ptr(), sb, sn, sh))
+
+    def _bhnd(self, t, name, batch, n, heads):
+        """ac_tensor of a [batch, heads, n, d] view."""
+        if t.dtype != self.dtype or t.device != self.device or t.shape != (batch, heads, n, self.d):
+            self._refuse(t, name, (batch, heads, n, self.d))
+        sb, sh, sn, one = t.stride()
+        if one != 1:
+            raise ValueError(f"{name}: the last dimension must be contiguous")
+        return byref(_abi.ac_tensor(t.data_ptr(), sb, sn, sh))
+
+    def _refuse(self, t, name, shape):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {self.dtype} {shape} on {self.device}")
 
     def _plain(self, t, name, dtype, shape):
-        """Pointer of a contiguous tensor (None: NULL)."""
-        if t is None:
-            return None
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+        """Pointer of a contiguous tensor."""
+        if t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {shape} "
                              f"on {self.device}")
         return t.data_ptr()
 
     def _w(self, t, name):
-        return self._plain(t, name, self.w_dtype, (self.d,))
+        return None if t is None else self._plain(t, name, self.w_dtype, (self.d,))
 
     def _table(self, t):
         if t is None:
             if self.axes:
                 raise ValueError("table: this layer rotates, pass the tensor of ac_rope_table()")
             return None
-        nb = ctypes.c_size_t()
-        check("ac_rope_table_size", self.lib.ac_rope_table_size(self._layer, byref(nb)))
-        return self._plain(t, "table", torch.float32, (nb.value // 8, 2))
+        return self._plain(t, "table", torch.float32, (self._pairs, 2))
 
     def _pos(self, t, batch, n):
         """Pointer and batch stride of [n, axes] or [batch, n, axes] positions."""
@@ -154,15 +178,18 @@ class AttnLayer:
         device).  Tensors used on another stream than the current one are
         recorded there, so that freeing them does not hand their memory out
         while the call runs."""
-        with torch.cuda.device(self.device):
-            current = torch.cuda.current_stream()
-            if stream is None:
-                stream = current
-            elif stream != current:
-                for t in tensors:
-                    if t is not None:
-                        t.record_stream(stream)
-            check(fn, getattr(self.lib, fn)(self._layer, *args, stream.cuda_stream))
+        if torch._C._cuda_getDevice() != self._index:
+            with torch.cuda.device(self.device):
+                return self._call(fn, stream, tensors, *args)
+        raw = torch._C._cuda_getCurrentRawStream(self._index)
+        if stream is not None and stream.cuda_stream != raw:
+            raw = stream.cuda_stream
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+        code = getattr(self.lib, fn)(self._layer, *args, raw)
+        if code:
+            check(fn, code)
 
     def get_status(self, stream=None) -> int:
         with torch.cuda.device(self.device):
@@ -173,9 +200,9 @@ class AttnLayer:
     def ac_rope_table(self, stream=None):
         """The layer's cosines and sines, [pairs of all axes, 2] fp32: made once,
         passed to the calls below."""
-        nb = ctypes.c_size_t()
-        check("ac_rope_table_size", self.lib.ac_rope_table_size(self._layer, byref(nb)))
-        table = torch.empty(nb.value // 8, 2, dtype=torch.float32, device=self.device)
+        if not self.axes:
+            check("ac_rope_table", _abi.AC_ERR_UNSUPPORTED)
+        table = torch.empty(self._pairs, 2, dtype=torch.float32, device=self.device)
         self._call("ac_rope_table", stream, (table,), table.data_ptr())
         return table
 
@@ -189,25 +216,25 @@ class AttnLayer:
         ref = q if q is not None else k
         if ref is None or ref.dim() != 4:
             raise ValueError("ac_qk_norm_rope: q or k [batch, n, heads, d] is required")
-        batch, n = ref.shape[:2]
-        table_p = self._table(table)
+        batch, n, _, d = ref.shape
+        xq = yq = xk = yk = None
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty(batch, self.heads, n, d, dtype=self.dtype, device=self.device)
+            xq, yq = self._bnhd(q, "q", batch, n, self.heads), self._bhnd(q_out, "q_out", batch, n, self.heads)
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty(batch, self.kv_heads, n, d, dtype=self.dtype, device=self.device)
+            xk, yk = self._bnhd(k, "k", batch, n, self.kv_heads), self._bhnd(k_out, "k_out", batch, n, self.kv_heads)
+        elif k_out is not None:
+            raise ValueError("k_out without k")
         pos_p, pos_stride = self._pos(pos, batch, n)
-        args, outs = [], []
-        for x, w, b, y, heads, name in ((q, w_q, b_q, q_out, self.heads, "q"), (k, w_k, b_k, k_out, self.kv_heads, "k")):
-            if x is None:
-                if y is not None:
-                    raise ValueError(f"{name}_out without {name}")
-                args += [None, None, None, None]
-            else:
-                xv = self._view(x, name, (batch, n), heads)
-                if y is None:
-                    y = torch.empty(batch, heads, n, self.d, dtype=self.dtype, device=self.device)
-                args += [byref(xv), self._w(w, "w_" + name), self._w(b, "b_" + name),
-                         byref(self._view(y.transpose(1, 2), name + "_out", (batch, n), heads))]
-            outs.append(y)
-        self._call("ac_qk_norm_rope", stream, (q, k, table, pos, w_q, w_k, b_q, b_k, *outs), batch, n, table_p, pos_p,
-                   pos_stride, *args)
-        return tuple(outs)
+        self._call("ac_qk_norm_rope", stream, (q, k, table, pos, w_q, w_k, b_q, b_k, q_out, k_out), batch, n,
+                   self._table(table), pos_p, pos_stride, xq, self._w(w_q, "w_q"), self._w(b_q, "b_q"), yq, xk,
+                   self._w(w_k, "w_k"), self._w(b_k, "b_k"), yk)
+        return q_out, k_out
 
     def ac_qk_norm_rope_backward(self, gq, gk, q=None, k=None, table=None, pos=None, w_q=None, w_k=None, b_q=None,
                                  b_k=None, dq=None, dk=None, stream=None):
@@ -219,37 +246,34 @@ class AttnLayer:
         if ref is None or ref.dim() != 4:
             raise ValueError("ac_qk_norm_rope_backward: gq or gk [batch, heads, n, d] is required")
         batch, n = ref.shape[0], ref.shape[2]
-        norm = self.cfg.norm != "none"
-        table_p = self._table(table)
         pos_p, pos_stride = self._pos(pos, batch, n)
-        args, res, used = [], {}, []
-        for g, x, w, b, dx, heads, name in ((gq, q, w_q, b_q, dq, self.heads, "q"),
-                                            (gk, k, w_k, b_k, dk, self.kv_heads, "k")):
-            dw = db = None
-            if g is None:
-                if dx is not None:
-                    raise ValueError(f"d{name} without g{name}")
-                args += [None] * 6
-            else:
-                if norm and x is None:
-                    raise ValueError(f"{name}: the norm's gradient needs the forward call's input")
-                gv = self._view(g.transpose(1, 2), "g" + name, (batch, n), heads)
-                if dx is None:
-                    dx = torch.empty(batch, n, heads, self.d, dtype=self.dtype, device=self.device)
-                if norm:
-                    xv = byref(self._view(x, name, (batch, n), heads))
-                    dw, db = (None if p is None else torch.empty(self.d, dtype=self.w_dtype, device=self.device)
-                              for p in (w, b))
-                else:
-                    xv = None
-                args += [byref(gv), xv, self._w(w, "w_" + name), byref(self._view(dx, "d" + name, (batch, n), heads)),
-                         None if dw is None else dw.data_ptr(), None if db is None else db.data_ptr()]
+        aq, rq = self._back_args(gq, q, w_q, b_q, dq, batch, n, self.heads, "q")
+        ak, rk = self._back_args(gk, k, w_k, b_k, dk, batch, n, self.kv_heads, "k")
+        self._call("ac_qk_norm_rope_backward", stream, (gq, q, w_q, *rq, gk, k, w_k, *rk, table, pos, self.ws), batch,
+                   n, self._table(table), pos_p, pos_stride, *aq, *ak, self._ws_ptr, self._ws_have)
+        return {"q": rq[0], "w_q": rq[1], "b_q": rq[2], "k": rk[0], "w_k": rk[1], "b_k": rk[2]}
+
+    def _back_args(self, g, x, w, b, dx, batch, n, heads, name):
+        """One tensor's arguments of the backward call, and its (dx, dw, db)."""
+        if g is None:
+            if dx is not None:
+                raise ValueError(f"d{name} without g{name}")
+            return (None,) * 6, (None, None, None)
+        xv = dw = db = None
+        if self.normed:
+            if x is None:
+                raise ValueError(f"{name}: the norm's gradient needs the forward call's input")
+            xv = self._bnhd(x, name, batch, n, heads)
+            if w is not None:
+                dw = torch.empty(self.d, dtype=self.w_dtype, device=self.device)
+            if b is not None:
                 self._w(b, "b_" + name)
-            res.update({name: dx, "w_" + name: dw, "b_" + name: db})
-            used += [g, x, w, dx, dw, db]
-        self._call("ac_qk_norm_rope_backward", stream, (*used, table, pos, self.ws), batch, n, table_p, pos_p,
-                   pos_stride, *args, self.ws.data_ptr(), self._ws_have)
-        return res
+                db = torch.empty(self.d, dtype=self.w_dtype, device=self.device)
+        if dx is None:
+            dx = torch.empty(batch, n, heads, self.d, dtype=self.dtype, device=self.device)
+        return ((self._bhnd(g, "g" + name, batch, n, heads), xv, self._w(w, "w_" + name),
+                 self._bnhd(dx, "d" + name, batch, n, heads), None if dw is None else dw.data_ptr(),
+                 None if db is None else db.data_ptr()), (dx, dw, db))
 
     def _cache(self, tokens, k_pages, v_pages, block_table, q_start, kv_len):
         """The arguments that both cache calls share."""
@@ -272,21 +296,20 @@ class AttnLayer:
         tokens = k.shape[0]
         seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
                                                                         q_start, kv_len)
-        table_p = self._table(table)
-        pos_p = self._plain(pos, "pos", torch.int32, (tokens, self.axes))
+        pos_p = None if pos is None else self._plain(pos, "pos", torch.int32, (tokens, self.axes))
         qv = qo = None
         if q is not None:
-            qv = byref(self._view(q, "q", (tokens,), self.heads))
+            qv = self._rows(q, "q", tokens, self.heads)
             if q_out is None:
                 q_out = torch.empty(tokens, self.heads, self.d, dtype=self.dtype, device=self.device)
-            qo = byref(self._view(q_out, "q_out", (tokens,), self.heads))
+            qo = self._rows(q_out, "q_out", tokens, self.heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
         self._call("ac_cache_append", stream,
                    (k, v, k_pages, v_pages, block_table, q_start, kv_len, q, table, pos, w_q, w_k, b_q, b_k, q_out),
-                   seqs, tokens, qs, kl, bt, max_pages, num_pages, table_p, pos_p,
-                   byref(self._view(k, "k", (tokens,), self.kv_heads)), self._w(w_k, "w_k"), self._w(b_k, "b_k"),
-                   byref(self._view(v, "v", (tokens,), self.kv_heads)), kp, vp, qv, self._w(w_q, "w_q"),
+                   seqs, tokens, qs, kl, bt, max_pages, num_pages, self._table(table), pos_p,
+                   self._rows(k, "k", tokens, self.kv_heads), self._w(w_k, "w_k"), self._w(b_k, "b_k"),
+                   self._rows(v, "v", tokens, self.kv_heads), kp, vp, qv, self._w(w_q, "w_q"),
                    self._w(b_q, "b_q"), qo)
         return q_out
 
@@ -306,7 +329,7 @@ class AttnLayer:
         self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
                    seqs, tokens, tokens if max_q is None else int(max_q),
                    max_pages * self.cfg.page_size if max_kv is None else int(max_kv), qs, kl, bt, max_pages, num_pages,
-                   byref(self._view(q, "q", (tokens,), self.heads)), kp, vp,
-                   byref(self._view(out, "out", (tokens,), self.heads)), None if lse_t is None else lse_t.data_ptr(),
-                   self.ws.data_ptr(), self._ws_have)
+                   self._rows(q, "q", tokens, self.heads), kp, vp,
+                   self._rows(out, "out", tokens, self.heads), None if lse_t is None else lse_t.data_ptr(),
+                   self._ws_ptr, self._ws_have)
         return (out, lse_t) if lse else out
