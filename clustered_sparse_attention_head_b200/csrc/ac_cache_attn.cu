@@ -49,8 +49,12 @@ template <int D> struct CCfg {
     static constexpr int OFF_K = 2 * Q_BYTES;
     static constexpr int OFF_V = OFF_K + KST * KV_BYTES;
     static constexpr int OFF_BAR = OFF_V + VST * KV_BYTES;
-    static constexpr int OFF_X = OFF_BAR + 512;     // (max, sum) of tile 1 per row, when tiles share rows
-    static constexpr int SMEM_RAW = OFF_X + 128 * 8 + 1024;
+    static constexpr int OFF_X = OFF_BAR + 448;     // (max, sum) of tile 1 per row, when tiles share rows
+    static constexpr int OFF_SCHED = OFF_X + 128 * 8;  // ring of scheduled units
+    static constexpr int SCHED = 4;                 // its depth
+    static constexpr int SMEM_RAW = OFF_SCHED + 4 * SCHED + 1024;
+    // threads that read each ring entry: V producer warp, MMA warp, both softmax warpgroups
+    static constexpr int SCHED_READERS = 32 + 32 + 256;
     // at least 116 KB so that two CTAs never share an SM (each takes all of TMEM)
     static constexpr int SMEM = SMEM_RAW > 116 * 1024 ? SMEM_RAW : 116 * 1024;
     // warps 0-3 softmax tile 0, 4-7 softmax tile 1, 8 TMA (Q, K), 9 MMA, 10 TMA (V), 11 idle
@@ -71,6 +75,8 @@ struct Plan {
     int whole;     // items taken whole: units 0 .. whole - 1
     int nsplit;    // pieces of each later item
     int units;
+    int *next;           // units handed out beyond the CTAs' first ones (0 between calls)
+    unsigned *done;      // CTAs that are through (0 between calls)
     float *part_o;   // [units - whole, 256, D]
     float2 *part_ml; // [units - whole, 256]
 };
@@ -211,7 +217,9 @@ __global__ void __launch_bounds__(384, 1)
     uint64_t *o_done = o_free + 2;        // [tile]: one phase per unit, after its last P.V
     uint64_t *xchg = o_done + 2;          // shared rows: tile 1's (max, sum) written; 128 arrivals
     uint64_t *comb_done = xchg + 1;       // shared rows: tile 0 has read O_1; 128 arrivals
-    uint64_t *drain_bar = comb_done + 1;
+    uint64_t *sched_full = comb_done + 1;           // [SCHED], 1 arrival
+    uint64_t *sched_empty = sched_full + C::SCHED;  // [SCHED], SCHED_READERS arrivals
+    uint64_t *drain_bar = sched_empty + C::SCHED;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain_bar + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(drain_bar + 2);
 
@@ -235,6 +243,10 @@ __global__ void __launch_bounds__(384, 1)
         }
         mbar_init(xchg, 128);
         mbar_init(comb_done, 128);
+        for (int i = 0; i < C::SCHED; i++) {
+            mbar_init(sched_full + i, 1);
+            mbar_init(sched_empty + i, C::SCHED_READERS);
+        }
         mbar_init(drain_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -252,6 +264,41 @@ __global__ void __launch_bounds__(384, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // CTA i begins with unit i.  The others are handed out as CTAs get free: the
+    // TMA warp draws the next one from a counter and publishes it in a shared
+    // ring, which every other role reads in the same order (-1 ends it).
+    const bool dealt = pl.units > (int)gridDim.x;
+    volatile int *sched_ring = reinterpret_cast<volatile int *>(sm + C::OFF_SCHED);
+    uint32_t sched_pos = 0;
+    // the next unit for a reading role (whole warp or warpgroup); -2 on abort
+    auto unit_after = [&]() -> int {
+        if (!dealt) return -1;
+        const int qs = (int)(sched_pos % C::SCHED);
+        if (!mbar_wait_warp(sched_full + qs, (sched_pos / C::SCHED) & 1, abort_flag, a.status)) return -2;
+        const int unit = sched_ring[qs];
+        mbar_arrive(sched_empty + qs);
+        sched_pos++;
+        return unit;
+    };
+    // ... and for the TMA warp
+    auto unit_drawn = [&]() -> int {
+        if (!dealt) return -1;
+        int unit = 0;
+        if (lane == 0) unit = atomicAdd(pl.next, 1) + (int)gridDim.x;
+        unit = __shfl_sync(0xffffffffu, unit, 0);
+        if (unit >= pl.units) unit = -1;
+        const int qs = (int)(sched_pos % C::SCHED);
+        if (sched_pos >= (uint32_t)C::SCHED &&
+            !mbar_wait_warp(sched_empty + qs, ((sched_pos / C::SCHED) - 1) & 1, abort_flag, a.status))
+            return -2;
+        if (lane == 0) {
+            sched_ring[qs] = unit;
+            mbar_arrive(sched_full + qs);
+        }
+        __syncwarp();
+        sched_pos++;
+        return unit;
+    };
 
     if (warp >= 8) {
     regs_dec3<C::REGS_LOW>();
@@ -272,7 +319,10 @@ __global__ void __launch_bounds__(384, 1)
         int slot = 0;
         uint32_t phase = 0;
         bool ok = true;
-        for (int u = blockIdx.x; u < pl.units && ok; u += gridDim.x) {
+        for (int u = blockIdx.x, next_u; u >= 0 && ok; u = next_u) {
+            // drawn ahead of the unit's loads: the other roles need not wait for it
+            next_u = kq ? unit_drawn() : unit_after();
+            if (next_u == -2) { ok = false; break; }
             const Unit w = decode(a, pl, u, kq && lane == 0);
             if (!w.nq || !w.nch) continue;
             if (kq) {
@@ -350,7 +400,9 @@ __global__ void __launch_bounds__(384, 1)
                 vph ^= 1u;
             }
         };
-        for (int u = blockIdx.x; u < pl.units; u += gridDim.x) {
+        for (int u = blockIdx.x, next_u; u >= 0; u = next_u) {
+            next_u = unit_after();
+            if (next_u == -2) { ok = false; break; }
             const Unit w = decode(a, pl, u, false);
             if (!w.nq || !w.nch) continue;
             const int nt = w.nt;
@@ -450,6 +502,8 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 9) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
+        // the last CTA of the call puts the counters back to 0 (atomicInc wraps)
+        if (dealt && lane == 0 && atomicInc(pl.done, gridDim.x - 1) == gridDim.x - 1) atomicExch(pl.next, 0);
     }
     } else {
         regs_inc3<C::REGS_HIGH>();
@@ -468,7 +522,9 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t shares = 0;      // units with shared rows (= xchg / comb_done phases) so far
         float2 *xs = reinterpret_cast<float2 *>(sm + C::OFF_X);
         bool ok = true;
-        for (int u = blockIdx.x; u < pl.units; u += gridDim.x) {
+        for (int u = blockIdx.x, next_u; u >= 0; u = next_u) {
+            next_u = unit_after();
+            if (next_u == -2) { ok = false; break; }
             const Unit w = decode(a, pl, u, false);
             if (!w.nq) continue;
             const bool share = !w.two && w.nt == 2;
@@ -719,7 +775,8 @@ bool encode(void *fn, CUtensorMap *m, const void *base, int rank, const cuuint64
                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int max_slots(int num_sms) { return 2 * num_sms; }
+constexpr int FILL = 2;
+int max_slots(int num_sms) { return 2 * FILL * num_sms; }
 
 template <int D> int launch(const CacheAttnArgs &a, const Plan &pl, int num_sms, void *encode_fn, cudaStream_t st) {
     using C = CCfg<D>;
@@ -779,14 +836,19 @@ int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStrea
     if (items > 0x3fffffffLL) return -1;
     // Whole items for the full waves over the SMs; the items left over are cut
     // into the number of pieces whose waves take least: a wave of pieces costs
-    // their chunks plus about 3 chunks' time to start and to write out.
+    // their chunks plus about 3 chunks' time to start and to write out.  With
+    // several sequences the items differ in length and CTAs get free at different
+    // times: then the last num_sms items or more are cut in pieces too, small
+    // enough to fill the gaps.
     long long keys = a.max_kv;
     if (a.window) keys = std::min<long long>(keys, (long long)a.window + 2 * pl.tpt + a.causal_block);
     const int chunks = (int)((keys + CHUNK - 1) / CHUNK);
-    const int left = (int)(items % num_sms);
-    pl.whole = (int)(items - left);
+    int left = (int)(items % num_sms);
     pl.nsplit = 1;
-    if (left) {
+    if (a.seqs > 1 && items >= num_sms && chunks >= 4 * FILL) {
+        left = std::min((int)items, left + num_sms);
+        pl.nsplit = FILL;
+    } else if (left) {
         double best = 1e30;
         for (int n = 1; n <= std::max(1, chunks) && left * n <= max_slots(num_sms); n++) {
             const double cost = (double)((left * n + num_sms - 1) / num_sms) * ((chunks + n - 1) / n + (n > 1 ? 3 : 0));
@@ -796,7 +858,10 @@ int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStrea
             }
         }
     }
+    pl.whole = (int)(items - left);
     pl.units = pl.whole + left * pl.nsplit;
+    pl.next = a.counters;
+    pl.done = (unsigned *)(a.counters + 1);
     pl.part_o = (float *)a.ws;
     pl.part_ml = (float2 *)((char *)a.ws + (size_t)max_slots(num_sms) * 256 * a.D * sizeof(float));
     return a.D == 64 ? launch<64>(a, pl, num_sms, encode_fn, st) : launch<128>(a, pl, num_sms, encode_fn, st);

@@ -447,6 +447,7 @@ ac_status ac_cache_attn(ac_layer *l, int seqs, int tokens, int max_q, int max_kv
     a.vp = v_pages;
     a.lse = lse;
     a.status = l->d_status;
+    a.counters = l->d_status + 2;
     a.ws = ws;
     if (k_cache_attn(a, l->num_sms, l->encode_fn, (cudaStream_t)stream)) return AC_ERR_UNSUPPORTED;
     return leave();

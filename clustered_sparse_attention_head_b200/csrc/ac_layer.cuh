@@ -114,6 +114,7 @@ struct CacheAttnArgs {
     const void *kp, *vp;
     float *lse;
     int *status;
+    int *counters;     // two words of the layer, 0 between calls
     void *ws;
 };
 // the kernel's attributes on the current device: once per layer

@@ -365,8 +365,9 @@ AC_API const char *ac_status_string(ac_status s);
  *    table) are recorded in the layer's status word (ac_layer_get_status).
  *  - The current device must be the one the layer was created on
  *    (AC_ERR_INVALID_ARG otherwise).
- *  - Calls that take a workspace must not overlap on the GPU with another call
- *    that uses the same workspace; the calls without one may overlap.
+ *  - Calls that take a workspace must not overlap on the GPU with one another
+ *    when they share the workspace or the layer (ac_cache_attn hands out its
+ *    work through counters of the layer); the calls without one may overlap.
  *  - No call synchronises or allocates, so each can be captured into a CUDA
  *    graph; everything that changes from step to step (lengths, positions,
  *    block table) is read from device memory.
