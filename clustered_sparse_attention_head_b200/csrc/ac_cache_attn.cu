@@ -32,7 +32,7 @@
 // its copies and MMAs, frees TMEM and returns.
 #include <algorithm>
 
-#include "ac_layer.cuh"
+#include "ac_cache.cuh"
 #include "ac_softmax.cuh"
 
 namespace ac {
@@ -93,38 +93,6 @@ struct Unit {
     bool two;        // two tiles of rows (else both tiles share one)
     int nc0, nc1;    // chunks of tile 0 / tile 1
 };
-
-// Keys [lo, hi) that a token at position p sees of a sequence of `len` keys.
-__device__ __forceinline__ void key_range(const CacheAttnArgs &a, int p, int len, int &lo, int &hi) {
-    hi = len;
-    lo = 0;
-    if (a.causal_block) {
-        const long long e = p < 0 ? 0 : ((long long)(p / a.causal_block) + 1) * a.causal_block;
-        hi = (int)min((long long)len, e);
-    }
-    if (a.window) lo = (int)max(0LL, (long long)p - a.window + 1);
-}
-
-// Sequence s: its rows (cut to the tensor and to max_q), the position of its
-// first new token and its keys.
-__device__ __forceinline__ void sequence(const CacheAttnArgs &a, int s, int &row0, int &nq, int &p0, int &len, bool report) {
-    const int s0 = __ldg(a.q_start + s), s1 = __ldg(a.q_start + s + 1);
-    len = __ldg(a.kv_len + s);
-    p0 = len - (s1 - s0);
-    row0 = max(0, s0);
-    nq = max(0, min(s1, a.tokens) - row0);
-    p0 += row0 - s0;
-    bool bad = s0 < 0 || s1 > a.tokens || s1 < s0;
-    if (nq > a.max_q) {
-        nq = a.max_q;
-        bad = true;
-    }
-    if (len < 0 || len > a.max_kv) {
-        len = len < 0 ? 0 : a.max_kv;
-        bad = true;
-    }
-    if (bad && report) set_status(a.status, ST_INVALID);
-}
 
 __device__ __forceinline__ Unit decode(const CacheAttnArgs &a, const Plan &pl, int u, bool report) {
     Unit w;
@@ -194,9 +162,6 @@ __device__ __forceinline__ void tma_load_3d_hint_p(uint32_t leader, void *dst, c
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy), "r"(leader)
         : "memory");
 }
-
-// 2^(a - b), 0 for a = -inf also when b is
-__device__ __forceinline__ float weight(float a, float b) { return a == -INFINITY ? 0.f : ex2_approx(a - b); }
 
 template <int D>
 __global__ void __launch_bounds__(384, 1)
@@ -726,6 +691,7 @@ template <int D>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ CacheAttnArgs a, const __grid_constant__ Plan pl,
                                                     int items, int rows) {
     constexpr int E = D / 32;
+    after_previous();
     const int lane = threadIdx.x & 31;
     const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int it = (int)(w / rows), r = (int)(w - (long long)it * rows);
@@ -801,8 +767,7 @@ template <int D> int launch(const CacheAttnArgs &a, const Plan &pl, int num_sms,
     if (pl.nsplit > 1) {
         const int items = (pl.units - pl.whole) / pl.nsplit;
         const int rows = std::min(2 * pl.tpt, a.max_q) * a.group;
-        merge_kernel<D><<<(unsigned)(((long long)items * rows + 7) / 8), 256, 0, st>>>(a, pl, items, rows);
-        note_launch();
+        launch_after(merge_kernel<D>, (unsigned)(((long long)items * rows + 7) / 8), 256, st, a, pl, items, rows);
     }
     return 0;
 }
@@ -821,7 +786,10 @@ template <int D> int setup() {
 
 }  // namespace
 
-int cache_attn_setup(int D) { return D == 64 ? setup<64>() : setup<128>(); }
+int cache_attn_setup(int D) {
+    if (cache_decode_setup(D)) return -1;
+    return D == 64 ? setup<64>() : setup<128>();
+}
 
 size_t cache_attn_ws(int num_sms, int D) {
     return (size_t)max_slots(num_sms) * 256 * (D * sizeof(float) + sizeof(float2));
@@ -829,6 +797,8 @@ size_t cache_attn_ws(int num_sms, int D) {
 
 int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStream_t st) {
     if (a.group > 128) return -1;
+    const int cs = decode_cluster(a, num_sms);
+    if (cs) return k_cache_decode(a, cs, st);
     Plan pl;
     pl.tpt = 128 / a.group;
     pl.blocks = (a.max_q + 2 * pl.tpt - 1) / (2 * pl.tpt);

@@ -94,6 +94,24 @@ struct FreqArgs {
     double mag;
 };
 
+// A kernel that reads what the one before it on the stream wrote, launched while
+// that one still runs: it begins with after_previous(), which waits for it.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+void launch_after(void (*fn)(P...), unsigned grid, unsigned block, cudaStream_t st, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute at[1];
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.stream = st;
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    // an error stays pending for the caller's check
+    if (cudaLaunchKernelEx(&cfg, fn, P(args)...) == cudaSuccess) note_launch();
+}
+
 // ---- ac_rope.cu
 void k_rope_table(const RopeArgs &r, const FreqArgs &f, float2 *table, cudaStream_t st);
 // the forward kernel's shared-memory attribute on the current device: once per layer

@@ -607,6 +607,7 @@ __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __g
 // Block (tensor, dw or db): the CTAs' partial sums in order, in double.
 __global__ void __launch_bounds__(1024) back_sum_kernel(const __grid_constant__ BackArgs a, int D) {
     __shared__ double red[1024];
+    after_previous();
     const int ti = blockIdx.x >> 1, which = blockIdx.x & 1;
     const BackTensor &t = a.t[ti];
     void *out = which ? t.db : t.dw;
@@ -736,8 +737,7 @@ int k_norm_rope_back(BackArgs &a, int dtype, int D, int num_sms, cudaStream_t st
     fn<<<a.ctas[0] + a.ctas[1], NT, back_smem(stat), st>>>(a);
     note_launch();
     if (a.part) {
-        back_sum_kernel<<<4, 1024, 0, st>>>(a, D);
-        note_launch();
+        launch_after(back_sum_kernel, 4, 1024, st, a, D);
     }
     return 0;
 }

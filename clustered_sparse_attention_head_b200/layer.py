@@ -86,6 +86,7 @@ class AttnLayer:
         with torch.cuda.device(self.device):
             check("ac_layer_create", self.lib.ac_layer_create(byref(c), byref(self._layer)))
         self.heads, self.kv_heads, self.d, self.axes = c.heads, c.kv_heads, c.d, c.rope_axes
+        self._w_shape = (c.d,)
         self.normed = c.norm != _abi.AC_NORM_NONE
         self.dtype, self.w_dtype = _DTYPES[cfg.dtype][1], _DTYPES[cfg.w_dtype][1]
         self._index = self.device.index
@@ -156,7 +157,11 @@ class AttnLayer:
         return t.data_ptr()
 
     def _w(self, t, name):
-        return None if t is None else self._plain(t, name, self.w_dtype, (self.d,))
+        if t is None:
+            return None
+        if t.dtype != self.w_dtype or t.device != self.device or t.shape != self._w_shape or t.stride() != (1,):
+            return self._plain(t, name, self.w_dtype, self._w_shape)
+        return t.data_ptr()
 
     def _table(self, t):
         if t is None:
@@ -220,13 +225,13 @@ class AttnLayer:
         xq = yq = xk = yk = None
         if q is not None:
             if q_out is None:
-                q_out = torch.empty(batch, self.heads, n, d, dtype=self.dtype, device=self.device)
+                q_out = q.new_empty((batch, self.heads, n, d))
             xq, yq = self._bnhd(q, "q", batch, n, self.heads), self._bhnd(q_out, "q_out", batch, n, self.heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if k is not None:
             if k_out is None:
-                k_out = torch.empty(batch, self.kv_heads, n, d, dtype=self.dtype, device=self.device)
+                k_out = k.new_empty((batch, self.kv_heads, n, d))
             xk, yk = self._bnhd(k, "k", batch, n, self.kv_heads), self._bhnd(k_out, "k_out", batch, n, self.kv_heads)
         elif k_out is not None:
             raise ValueError("k_out without k")
@@ -247,14 +252,16 @@ class AttnLayer:
             raise ValueError("ac_qk_norm_rope_backward: gq or gk [batch, heads, n, d] is required")
         batch, n = ref.shape[0], ref.shape[2]
         pos_p, pos_stride = self._pos(pos, batch, n)
-        aq, rq = self._back_args(gq, q, w_q, b_q, dq, batch, n, self.heads, "q")
-        ak, rk = self._back_args(gk, k, w_k, b_k, dk, batch, n, self.kv_heads, "k")
+        sums = torch.empty(4, self.d, dtype=self.w_dtype, device=self.device).unbind() if self.normed else ()
+        aq, rq = self._back_args(gq, q, w_q, b_q, dq, sums[:2], batch, n, self.heads, "q")
+        ak, rk = self._back_args(gk, k, w_k, b_k, dk, sums[2:], batch, n, self.kv_heads, "k")
         self._call("ac_qk_norm_rope_backward", stream, (gq, q, w_q, *rq, gk, k, w_k, *rk, table, pos, self.ws), batch,
                    n, self._table(table), pos_p, pos_stride, *aq, *ak, self._ws_ptr, self._ws_have)
         return {"q": rq[0], "w_q": rq[1], "b_q": rq[2], "k": rk[0], "w_k": rk[1], "b_k": rk[2]}
 
-    def _back_args(self, g, x, w, b, dx, batch, n, heads, name):
-        """One tensor's arguments of the backward call, and its (dx, dw, db)."""
+    def _back_args(self, g, x, w, b, dx, sums, batch, n, heads, name):
+        """One tensor's arguments of the backward call, and its (dx, dw, db);
+        sums: where dw and db go."""
         if g is None:
             if dx is not None:
                 raise ValueError(f"d{name} without g{name}")
@@ -265,12 +272,12 @@ class AttnLayer:
                 raise ValueError(f"{name}: the norm's gradient needs the forward call's input")
             xv = self._bnhd(x, name, batch, n, heads)
             if w is not None:
-                dw = torch.empty(self.d, dtype=self.w_dtype, device=self.device)
+                dw = sums[0]
             if b is not None:
                 self._w(b, "b_" + name)
-                db = torch.empty(self.d, dtype=self.w_dtype, device=self.device)
+                db = sums[1]
         if dx is None:
-            dx = torch.empty(batch, n, heads, self.d, dtype=self.dtype, device=self.device)
+            dx = g.new_empty((batch, n, heads, self.d))
         return ((self._bhnd(g, "g" + name, batch, n, heads), xv, self._w(w, "w_" + name),
                  self._bnhd(dx, "d" + name, batch, n, heads), None if dw is None else dw.data_ptr(),
                  None if db is None else db.data_ptr()), (dx, dw, db))
@@ -301,7 +308,7 @@ class AttnLayer:
         if q is not None:
             qv = self._rows(q, "q", tokens, self.heads)
             if q_out is None:
-                q_out = torch.empty(tokens, self.heads, self.d, dtype=self.dtype, device=self.device)
+                q_out = q.new_empty((tokens, self.heads, self.d))
             qo = self._rows(q_out, "q_out", tokens, self.heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
@@ -324,7 +331,7 @@ class AttnLayer:
         seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
                                                                         q_start, kv_len)
         if out is None:
-            out = torch.empty(tokens, self.heads, self.d, dtype=self.dtype, device=self.device)
+            out = q.new_empty((tokens, self.heads, self.d))
         lse_t = torch.empty(tokens, self.heads, dtype=torch.float32, device=self.device) if lse else None
         self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
                    seqs, tokens, tokens if max_q is None else int(max_q),

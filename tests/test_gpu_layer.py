@@ -395,6 +395,10 @@ ATTN = [
     (40, 40, 128, 64, 8, 0, [8], [72]),
     (1, 1, 128, 16, 1, 1, [9], [30]),              # every token sees itself alone
     (16, 16, 64, 16, 1, 0, [1] * 9, [3, 0, 16, 17, 31, 128, 129, 255, 1000]),
+    (32, 8, 128, 32, 1, 0, [4, 1, 3, 0], [4, 900, 2500, 7]),   # 16 rows a key head
+    (16, 2, 64, 64, 0, 0, [2, 1], [5000, 33]),
+    (3, 1, 128, 16, 1, 37, [5, 4], [700, 40]),                 # 15 rows, windows that begin inside a block
+    (16, 1, 64, 16, 5, 0, [1], [4099]),
 ]
 
 
