@@ -73,6 +73,42 @@ class AcError(RuntimeError):
         self.code = code
 
 
+P, T = c_void_p, POINTER(ac_tensor)
+SIGNATURES = {
+    "ac_create": ([POINTER(ac_config), POINTER(c_void_p)], c_int),
+    "ac_destroy": ([P], None),
+    "ac_capacities": ([P, POINTER(c_int), POINTER(c_int)], c_int),
+    "ac_workspace_size": ([P, POINTER(c_size_t)], c_int),
+    "ac_cluster_q": ([P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_cluster_k": ([P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_select": ([P, P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_key_bounds": ([P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_select_rows": ([P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_sparse_attn_rows": ([P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_cluster_sort": ([P, P, c_int, P, P, P, P, c_size_t, P], c_int),
+    "ac_cluster_sort_static": ([P, c_int, c_int, c_int, P, P, P, P], c_int),
+    "ac_sparse_attn": ([P, P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
+    "ac_forward": ([P, P, P, P, P, P, P, POINTER(ac_stats), P, c_size_t, P], c_int),
+    "ac_step_state_size": ([P, POINTER(c_size_t)], c_int),
+    "ac_step_state_parts": ([P, P, P], c_int),
+    "ac_forward_step": ([P, c_int, P, P, P, P, P, POINTER(ac_stats), P, c_size_t, P], c_int),
+    "ac_profile_read": ([P, POINTER(ac_profile)], c_int),
+    "ac_get_status": ([P, P], c_int),
+    "ac_selftest_wait": ([P, c_double, P], c_int),
+    "ac_status_string": ([c_int], ctypes.c_char_p),
+    "ac_layer_create": ([POINTER(ac_layer_config), POINTER(P)], c_int),
+    "ac_layer_destroy": ([P], None),
+    "ac_layer_workspace_size": ([P, POINTER(c_size_t)], c_int),
+    "ac_layer_get_status": ([P, P], c_int),
+    "ac_rope_table_size": ([P, POINTER(c_size_t)], c_int),
+    "ac_rope_table": ([P, P, P], c_int),
+    "ac_qk_norm_rope": ([P, c_int, c_int, P, P, c_int64, T, P, P, T, T, P, P, T, P], c_int),
+    "ac_qk_norm_rope_backward": ([P, c_int, c_int, P, P, c_int64, T, T, P, T, P, P, T, T, P, T, P, P, P, c_size_t,
+                                  P], c_int),
+    "ac_cache_append": ([P, c_int, c_int, P, P, P, c_int, c_int, P, P, T, P, P, T, P, P, T, P, P, T, P], c_int),
+    "ac_cache_attn": ([P, c_int, c_int, c_int, c_int, P, P, P, c_int, c_int, T, P, P, T, P, P, c_size_t, P], c_int),
+}
+
 _lib = None
 
 
@@ -84,42 +120,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise RuntimeError(f"libadacluster.so not found at {path}; run __graft_entry__.build() first")
     lib = ctypes.CDLL(path)
-    P, T = c_void_p, POINTER(ac_tensor)
-    sig = {
-        "ac_create": ([POINTER(ac_config), POINTER(c_void_p)], c_int),
-        "ac_destroy": ([P], None),
-        "ac_capacities": ([P, POINTER(c_int), POINTER(c_int)], c_int),
-        "ac_workspace_size": ([P, POINTER(c_size_t)], c_int),
-        "ac_cluster_q": ([P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_cluster_k": ([P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_select": ([P, P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_key_bounds": ([P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_select_rows": ([P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_sparse_attn_rows": ([P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_cluster_sort": ([P, P, c_int, P, P, P, P, c_size_t, P], c_int),
-        "ac_cluster_sort_static": ([P, c_int, c_int, c_int, P, P, P, P], c_int),
-        "ac_sparse_attn": ([P, P, P, P, P, P, P, P, P, P, P, P, P, P, c_size_t, P], c_int),
-        "ac_forward": ([P, P, P, P, P, P, P, POINTER(ac_stats), P, c_size_t, P], c_int),
-        "ac_step_state_size": ([P, POINTER(c_size_t)], c_int),
-        "ac_step_state_parts": ([P, P, P], c_int),
-        "ac_forward_step": ([P, c_int, P, P, P, P, P, POINTER(ac_stats), P, c_size_t, P], c_int),
-        "ac_profile_read": ([P, POINTER(ac_profile)], c_int),
-        "ac_get_status": ([P, P], c_int),
-        "ac_selftest_wait": ([P, c_double, P], c_int),
-        "ac_status_string": ([c_int], ctypes.c_char_p),
-        "ac_layer_create": ([POINTER(ac_layer_config), POINTER(P)], c_int),
-        "ac_layer_destroy": ([P], None),
-        "ac_layer_workspace_size": ([P, POINTER(c_size_t)], c_int),
-        "ac_layer_get_status": ([P, P], c_int),
-        "ac_rope_table_size": ([P, POINTER(c_size_t)], c_int),
-        "ac_rope_table": ([P, P, P], c_int),
-        "ac_qk_norm_rope": ([P, c_int, c_int, P, P, c_int64, T, P, P, T, T, P, P, T, P], c_int),
-        "ac_qk_norm_rope_backward": ([P, c_int, c_int, P, P, c_int64, T, T, P, T, P, P, T, T, P, T, P, P, P, c_size_t,
-                                      P], c_int),
-        "ac_cache_append": ([P, c_int, c_int, P, P, P, c_int, c_int, P, P, T, P, P, T, P, P, T, P, P, T, P], c_int),
-        "ac_cache_attn": ([P, c_int, c_int, c_int, c_int, P, P, P, c_int, c_int, T, P, P, T, P, P, c_size_t, P], c_int),
-    }
-    for name, (args, res) in sig.items():
+    for name, (args, res) in SIGNATURES.items():
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res

@@ -439,6 +439,27 @@ def test_attn(case):
     _near(got2, ref, U.attend_tol(ref, absv, big), "default bounds")
 
 
+@pytest.mark.parametrize("d, heads, kv_heads, new, kv, block", [
+    (64, 40, 40, [300, 257], [2100, 2300], 1),      # more units than SMs, the last ones cut in pieces
+    (128, 20, 20, [513, 1], [1500, 700], 50),
+    (128, 2, 2, [1], [21000], 1),                   # a cluster of 16 CTAs
+    (64, 1, 1, [2], [60000], 0),                    # too few units for the GPU: tiles cut along the keys
+])
+def test_attn_many_units(d, heads, kv_heads, new, kv, block):
+    """Call after call the same bits, whichever CTA takes which unit, and right."""
+    lay = _layer(heads=heads, kv_heads=kv_heads, d=d, page_size=64, causal_block=block)
+    kp, vp, bt = _cache(lay, kv)
+    q = _rand(sum(new), heads, d, seed=7)
+    kvt = torch.tensor(kv, dtype=torch.int32).cuda()
+    args = (q, kp, vp, bt, _starts(new), kvt)
+    got = [lay.ac_cache_attn(*args, max_q=max(new), max_kv=max(kv)) for _ in range(3)]
+    assert lay.get_status() == 0
+    assert torch.equal(_bits(got[0]), _bits(got[1])) and torch.equal(_bits(got[0]), _bits(got[2]))
+    ref, _, absv, big, _ = U.attend(lay.cfg, q.double().cpu(), kp.double().cpu(), vp.double().cpu(), bt.cpu(),
+                                    _starts(new).cpu(), kv)
+    _near(got[0], ref, U.attend_tol(ref, absv, big), "out")
+
+
 def test_attn_large_scores_and_scale():
     """Scores in the hundreds whose maximum moves late, and a scale of its own."""
     lay = _layer(heads=2, d=64, page_size=16, causal_block=1, scale=0.37)
