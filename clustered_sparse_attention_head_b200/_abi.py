@@ -73,7 +73,7 @@ class AcError(RuntimeError):
         self.code = code
 
 
-P, T = c_void_p, POINTER(ac_tensor)
+P = T = c_void_p  # T: an ac_tensor
 SIGNATURES = {
     "ac_create": ([POINTER(ac_config), POINTER(c_void_p)], c_int),
     "ac_destroy": ([P], None),

@@ -9,6 +9,7 @@ the library's kernels.
 from __future__ import annotations
 
 import ctypes
+import struct
 from ctypes import byref, c_void_p
 from dataclasses import dataclass
 
@@ -22,6 +23,7 @@ _LAYOUTS = {"interleaved": _abi.AC_ROPE_INTERLEAVED, "half": _abi.AC_ROPE_HALF}
 _SCALINGS = {"none": _abi.AC_ROPE_PLAIN, "linear": _abi.AC_ROPE_LINEAR, "ntk": _abi.AC_ROPE_NTK,
              "yarn": _abi.AC_ROPE_YARN}
 _DTYPES = {"bf16": (_abi.AC_BF16, torch.bfloat16), "f32": (_abi.AC_F32, torch.float32)}
+_view = struct.Struct("Qqqq").pack  # an ac_tensor as bytes, which ctypes passes by address
 
 
 @dataclass
@@ -120,38 +122,39 @@ class AttnLayer:
     # The calls are a few microseconds on the GPU for few tokens, so these keep
     # to the cheapest forms that check everything.
     def _rows(self, t, name, tokens, heads):
-        """ac_tensor of a [tokens, heads, d] view."""
-        if t.dtype != self.dtype or t.device != self.device or t.shape != (tokens, heads, self.d):
+        """The ac_tensor of a [tokens, heads, d] view."""
+        if t.dtype != self.dtype or t.get_device() != self._index or t.shape != (tokens, heads, self.d):
             self._refuse(t, name, (tokens, heads, self.d))
         sn, sh, one = t.stride()
         if one != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        return byref(_abi.ac_tensor(t.data_ptr(), 0, sn, sh))
+        return _view(t.data_ptr(), 0, sn, sh)
 
     def _bnhd(self, t, name, batch, n, heads):
-        """ac_tensor of a [batch, n, heads, d] view."""
-        if t.dtype != self.dtype or t.device != self.device or t.shape != (batch, n, heads, self.d):
+        """... of a [batch, n, heads, d] view."""
+        if t.dtype != self.dtype or t.get_device() != self._index or t.shape != (batch, n, heads, self.d):
             self._refuse(t, name, (batch, n, heads, self.d))
         sb, sn, sh, one = t.stride()
         if one != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        return byref(_abi.ac_tensor(t.data_ptr(), sb, sn, sh))
+        return _view(t.data_ptr(), sb, sn, sh)
 
     def _bhnd(self, t, name, batch, n, heads):
-        """ac_tensor of a [batch, heads, n, d] view."""
-        if t.dtype != self.dtype or t.device != self.device or t.shape != (batch, heads, n, self.d):
+        """... of a [batch, heads, n, d] view."""
+        if t.dtype != self.dtype or t.get_device() != self._index or t.shape != (batch, heads, n, self.d):
             self._refuse(t, name, (batch, heads, n, self.d))
         sb, sh, sn, one = t.stride()
         if one != 1:
             raise ValueError(f"{name}: the last dimension must be contiguous")
-        return byref(_abi.ac_tensor(t.data_ptr(), sb, sn, sh))
+        return _view(t.data_ptr(), sb, sn, sh)
 
     def _refuse(self, t, name, shape):
-        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {self.dtype} {shape} on {self.device}")
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected {self.dtype} {shape} on "
+                         f"{self.device}")
 
     def _plain(self, t, name, dtype, shape):
         """Pointer of a contiguous tensor."""
-        if t.dtype != dtype or t.device != self.device or t.shape != shape or not t.is_contiguous():
+        if t.dtype != dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, expected contiguous {dtype} {shape} "
                              f"on {self.device}")
         return t.data_ptr()
@@ -159,7 +162,7 @@ class AttnLayer:
     def _w(self, t, name):
         if t is None:
             return None
-        if t.dtype != self.w_dtype or t.device != self.device or t.shape != self._w_shape or t.stride() != (1,):
+        if t.dtype != self.w_dtype or t.get_device() != self._index or t.shape != self._w_shape or t.stride() != (1,):
             return self._plain(t, name, self.w_dtype, self._w_shape)
         return t.data_ptr()
 
@@ -316,8 +319,7 @@ class AttnLayer:
                    (k, v, k_pages, v_pages, block_table, q_start, kv_len, q, table, pos, w_q, w_k, b_q, b_k, q_out),
                    seqs, tokens, qs, kl, bt, max_pages, num_pages, self._table(table), pos_p,
                    self._rows(k, "k", tokens, self.kv_heads), self._w(w_k, "w_k"), self._w(b_k, "b_k"),
-                   self._rows(v, "v", tokens, self.kv_heads), kp, vp, qv, self._w(w_q, "w_q"),
-                   self._w(b_q, "b_q"), qo)
+                   self._rows(v, "v", tokens, self.kv_heads), kp, vp, qv, self._w(w_q, "w_q"), self._w(b_q, "b_q"), qo)
         return q_out
 
     def ac_cache_attn(self, q, k_pages, v_pages, block_table, q_start, kv_len, max_q=None, max_kv=None, out=None,
@@ -336,7 +338,7 @@ class AttnLayer:
         self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
                    seqs, tokens, tokens if max_q is None else int(max_q),
                    max_pages * self.cfg.page_size if max_kv is None else int(max_kv), qs, kl, bt, max_pages, num_pages,
-                   self._rows(q, "q", tokens, self.heads), kp, vp,
-                   self._rows(out, "out", tokens, self.heads), None if lse_t is None else lse_t.data_ptr(),
+                   self._rows(q, "q", tokens, self.heads), kp, vp, self._rows(out, "out", tokens, self.heads),
+                   None if lse_t is None else lse_t.data_ptr(),
                    self._ws_ptr, self._ws_have)
         return (out, lse_t) if lse else out

@@ -522,6 +522,8 @@ AC_API ac_status ac_cache_append(ac_layer *layer, int seqs, int tokens, const in
  * recorded; a page id outside the pool is clamped and recorded.  Cache rows at
  * or beyond kv_len are never used, whatever they hold; rows before it must be
  * finite (a NaN or Inf value may reach every query of its sequence).
+ * max_q = 0: no sequence has new tokens, nothing is written.  At most 128 query
+ * heads per key head, and no broadcast q (a stride of 0): AC_ERR_UNSUPPORTED.
  * bf16 only (AC_ERR_UNSUPPORTED otherwise): products in bf16 with fp32
  * accumulation, softmax in fp32, its weights rounded to bf16 for the product
  * with v.                                                                     */
