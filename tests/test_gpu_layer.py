@@ -635,6 +635,60 @@ def test_graph_replay_with_new_lengths():
         assert (a[~seen.cuda()] == 4).all()
 
 
+def test_graph_of_every_call():
+    """Forward, gradients (two kernels), append and split attention (two kernels)
+    in one graph, replayed on new inputs."""
+    lay = _layer(heads=4, d=64, norm="layer", page_size=16, causal_block=1, rope_dims=(64,), rope_max=(4000,))
+    n = 600
+    kp, vp, bt = _cache(lay, [2900])
+    table = lay.ac_rope_table()
+    x = _rand(1, n, 12, 64, seed=2)
+    w, b = _rand(64, seed=3), _rand(64, seed=4)
+    st, kv = _starts([n]), torch.tensor([2900], dtype=torch.int32).cuda()
+
+    def step():
+        q, k = lay.ac_qk_norm_rope(x[:, :, :4], x[:, :, 4:8], table=table, w_q=w, w_k=w, b_q=b, b_k=b)
+        g = lay.ac_qk_norm_rope_backward(k, q, x[:, :, :4], x[:, :, 4:8], table=table, w_q=w, w_k=w, b_q=b, b_k=b)
+        qo = lay.ac_cache_append(x[0, :, 4:8], x[0, :, 8:], kp, vp, bt, st, kv, q=x[0, :, :4], table=table, w_q=w,
+                                 w_k=w)
+        return [q, k, *g.values(), qo, *lay.ac_cache_attn(qo, kp, vp, bt, st, kv, lse=True)]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = step()
+    for seed in (11, 12):
+        x.copy_(_rand(1, n, 12, 64, seed=seed))
+        graph.replay()
+        got = [t.clone() for t in outs]
+        want = step()
+        assert all(torch.equal(_bits(a), _bits(b)) for a, b in zip(got, want))
+    assert lay.get_status() == 0
+
+
+def test_calls_on_two_streams_at_once():
+    """Calls without a workspace may overlap, on one layer and its status word."""
+    lay = _layer(heads=16, d=128, norm="rms", rope_dims=(128,), rope_max=(9000,))
+    table = lay.ac_rope_table()
+    xs = [_rand(1, 8000, 32, 128, seed=i) for i in (1, 2)]
+    want = [lay.ac_qk_norm_rope(x[:, :, :16], x[:, :, 16:], table=table) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(5):
+        for i, (x, st) in enumerate(zip(xs, streams)):
+            with torch.cuda.stream(st):
+                got[i].append(lay.ac_qk_norm_rope(x[:, :, :16], x[:, :, 16:], table=table))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for pair in got[i] for a, b in zip(pair, want[i]))
+    assert lay.get_status() == 0
+
+
 def test_block_run_together():
     """A clip made three frames at a time: append and attention per chunk equal
     the 64-bit attention, causal by frames, of the whole clip's normed and
