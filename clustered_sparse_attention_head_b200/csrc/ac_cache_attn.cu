@@ -505,8 +505,9 @@ __global__ void __launch_bounds__(384, 1)
                     if (w.slot >= 0) {
                         pl.part_ml[(size_t)w.slot * 256 + k * 128 + row] = make_float2(-INFINITY, 0.f);
                     } else {
-                        uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out.p + (w.row0 + i) * a.out.sn +
-                                                               head * a.out.sh);
+                        uint4 *dst = reinterpret_cast<uint4 *>((__nv_bfloat16 *)a.out.p +
+                                                               (long long)(w.row0 + i) * a.out.sn +
+                                                               (long long)head * a.out.sh);
                         for (int x = 0; x < D / 8; x++) dst[x] = make_uint4(0u, 0u, 0u, 0u);
                         if (a.lse) a.lse[(long long)(w.row0 + i) * a.heads + head] = -INFINITY;
                     }
@@ -630,7 +631,8 @@ __global__ void __launch_bounds__(384, 1)
                 l = l * w0 + x.y * w1;
             }
             const int head = w.kvh * a.group + rhead;
-            __nv_bfloat16 *orow = (__nv_bfloat16 *)a.out.p + (w.row0 + tok) * a.out.sn + head * a.out.sh;
+            __nv_bfloat16 *orow = (__nv_bfloat16 *)a.out.p + (long long)(w.row0 + tok) * a.out.sn +
+                                  (long long)head * a.out.sh;
             const size_t prow = (size_t)w.slot * 256 + (w.two && t == 1 ? 128 : 0) + row;
             // a row without keys has l = 0 and O = 0
             const float inv = w.slot >= 0 ? 1.f : (l == 0.f ? 0.f : 1.f / l);
@@ -722,7 +724,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Cach
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     const int h = kvh * a.group + head;
-    __nv_bfloat16 *o = (__nv_bfloat16 *)a.out.p + (long long)(row0 + t) * a.out.sn + h * a.out.sh + lane * E;
+    __nv_bfloat16 *o = (__nv_bfloat16 *)a.out.p + (long long)(row0 + t) * a.out.sn + (long long)h * a.out.sh + lane * E;
 #pragma unroll
     for (int k = 0; k < E; k++) o[k] = __float2bfloat16(acc[k] * inv);
     if (a.lse && lane == 0)

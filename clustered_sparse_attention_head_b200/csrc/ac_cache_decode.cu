@@ -155,8 +155,8 @@ __global__ void __launch_bounds__(32 * WARPS, DCfg<D>::CTAS)
         const int tok = in ? r / a.group : 0;
         lo[h] = hi[h] = 0;
         if (in) key_range(a, p0 + tok, len, lo[h], hi[h]);
-        const __nv_bfloat16 *src = (const __nv_bfloat16 *)a.q.p + (row0 + tok) * a.q.sn +
-                                   (kvh * a.group + (in ? r - tok * a.group : 0)) * a.q.sh + (lane % 4) * 2;
+        const __nv_bfloat16 *src = (const __nv_bfloat16 *)a.q.p + (long long)(row0 + tok) * a.q.sn +
+                                   (long long)(kvh * a.group + (in ? r - tok * a.group : 0)) * a.q.sh + (lane % 4) * 2;
 #pragma unroll
         for (int k = 0; k < D / 16; k++) {
             q[k][h] = in ? __ldg((const uint32_t *)(src + k * 16)) : 0u;
@@ -315,7 +315,8 @@ __global__ void __launch_bounds__(32 * WARPS, DCfg<D>::CTAS)
         }
         const float inv = ll == 0.f ? 0.f : 1.f / ll;  // a row without keys: zeros
         const int tok = r / a.group, head = kvh * a.group + r - tok * a.group;
-        __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out.p + (row0 + tok) * a.out.sn + head * a.out.sh + c * 4;
+        __nv_bfloat16 *dst = (__nv_bfloat16 *)a.out.p + (long long)(row0 + tok) * a.out.sn +
+                             (long long)head * a.out.sh + c * 4;
         *reinterpret_cast<uint2 *>(dst) = make_uint2(bf2(acc.x * inv, acc.y * inv), bf2(acc.z * inv, acc.w * inv));
         if (a.lse && c == 0)
             a.lse[(long long)(row0 + tok) * a.heads + head] =

@@ -33,8 +33,9 @@ bool view_ok(const ac_tensor &t, long long batch, long long n, int heads, int d,
     int m = 0;
     for (int i = 0; i < 3; i++) {
         if (size[i] <= 1) continue;
-        // 2^40 elements: larger strides reach past any device and could overflow below
-        if (stride[i] < 0 || stride[i] > (1LL << 40) || (stride[i] * elt) % 16) return false;
+        // 2^40 elements reach past any device; token and head strides are 32-bit in
+        // the kernels (64-bit products cost the gradients' kernel 7%)
+        if (stride[i] < 0 || stride[i] > (i == 0 ? 1LL << 40 : 0x7fffffffLL) || (stride[i] * elt) % 16) return false;
         size[m] = size[i];
         stride[m++] = stride[i];
     }
@@ -73,7 +74,7 @@ bool alias_ok(const ac_tensor &x, const ac_tensor &y, long long batch, long long
     return xb <= ya || yb <= xa;
 }
 
-View view_of(const ac_tensor &t) { return View{t.data, t.batch_stride, t.token_stride, t.head_stride}; }
+View view_of(const ac_tensor &t) { return View{t.data, t.batch_stride, (int)t.token_stride, (int)t.head_stride}; }
 
 // The device check shared by every call that launches.
 ac_status enter(const ac_layer *l) {
@@ -382,7 +383,7 @@ ac_status ac_cache_append(ac_layer *l, int seqs, int tokens, const int32_t *q_st
     }
     const ac_status e = enter(l);
     if (e != AC_OK || !seqs || !tokens) return e;
-    const View kv{nullptr, 0, 0, (long long)l->cfg.page_size * d};
+    const View kv{nullptr, 0, 0, l->cfg.page_size * d};
     View kp = kv, vp = kv;
     kp.p = k_pages;
     vp.p = v_pages;

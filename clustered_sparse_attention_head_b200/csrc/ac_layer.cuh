@@ -5,10 +5,12 @@
 
 namespace ac {
 
-// [batch, token, head, d] view: data and strides in elements.
+// [batch, token, head, d] view: data and strides in elements (token and head
+// strides below 2^31).
 struct View {
     const void *p;
-    long long sb, sn, sh;
+    long long sb;
+    int sn, sh;
 };
 
 // n / d for 0 <= n < 2^31 by a multiplication: with l = ceil(log2 d) and m =

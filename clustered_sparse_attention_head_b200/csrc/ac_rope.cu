@@ -312,7 +312,7 @@ __global__ void __launch_bounds__(NT, FWD_CTAS) norm_rope_kernel(const __grid_co
     };
     auto load = [&](const Item &m, int slot) {
         const View &x = a.t[m.ti].x;
-        const T *p = (const T *)x.p + m.b * x.sb + m.i * x.sn + m.h0 * x.sh + e;
+        const T *p = (const T *)x.p + m.b * x.sb + (long long)m.i * x.sn + (long long)m.h0 * x.sh + e;
 #pragma unroll
         for (int j = 0; j < HC; j++) {
             if (j >= m.nh) break;
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(NT, FWD_CTAS) norm_rope_kernel(const __grid_co
         const RowTensor &t = a.t[m.ti];
         bool live = m.tok < tokens;
         int index = m.i;
-        long long at_y = m.b * t.y.sb + m.i * t.y.sn;
+        long long at_y = m.b * t.y.sb + (long long)m.i * t.y.sn;
         bool store = live;
         if (a.page.seqs) {
             int seq = 0, place = 0;
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(NT, FWD_CTAS) norm_rope_kernel(const __grid_co
                 }
             }
         }
-        T *y = (T *)t.y.p + at_y + m.h0 * t.y.sh + e;
+        T *y = (T *)t.y.p + at_y + (long long)m.h0 * t.y.sh + e;
         if (t.copy) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
@@ -470,8 +470,8 @@ __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __g
         lh = m.h0;
         lh1 = m.h1;
         llive = m.tok < tokens;
-        lg = (const T *)t.g.p + m.b * t.g.sb + m.i * t.g.sn + m.h0 * t.g.sh + e;
-        lx = (const T *)t.x.p + m.b * t.x.sb + m.i * t.x.sn + m.h0 * t.x.sh + e;
+        lg = (const T *)t.g.p + m.b * t.g.sb + (long long)m.i * t.g.sn + (long long)m.h0 * t.g.sh + e;
+        lx = (const T *)t.x.p + m.b * t.x.sb + (long long)m.i * t.x.sn + (long long)m.h0 * t.x.sh + e;
     };
     auto load_step = [&]() {
         if (lit < items) {
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __g
     for (int it = cta; it < items; it += a.ctas[ti]) {
         const Item m = item_of(it);
         const bool live = m.tok < tokens;
-        T *dx = (T *)t.dx.p + m.b * t.dx.sb + m.i * t.dx.sn + m.h0 * t.dx.sh + e;
+        T *dx = (T *)t.dx.p + m.b * t.dx.sb + (long long)m.i * t.dx.sn + (long long)m.h0 * t.dx.sh + e;
         Coef<V, HALF> turn;
         uint32_t on;
         {
@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __g
             on = ang.on;
             turn.template fold<true>(ang, a.rope, e / V, nullptr, nullptr);
         }
+        const bool full = __all_sync(0xffffffffu, on == Angles<V, HALF>::ALL);
         for (int h = m.h0; h < m.h1; h += HC) {
             load_step();
             asm volatile("cp.async.wait_group %0;" ::"n"(STEPS - 1) : "memory");
@@ -531,7 +532,10 @@ __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __g
                 const bool in = live;  // else g and x are zeros
                 f2 g[P];
                 Vec<T>::get(ring[at][j][threadIdx.x], g);
-                turn.template turn<false>(on, src, g);
+                if (full)
+                    turn.template turn<true>(on, src, g);
+                else
+                    turn.template turn<false>(on, src, g);
                 if (STAT) {
                     f2 x[P], s1 = 0, s2 = 0;
                     Vec<T>::get(ring[at][(HC + j) % PER][threadIdx.x], x);

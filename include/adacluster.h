@@ -424,7 +424,8 @@ typedef struct {
 
 /* A [batch, token, head, d] view of device memory: strides in elements, the d
  * elements of a head contiguous.  `data` 16-byte aligned and every stride a
- * multiple of 16 bytes (of a dimension longer than 1).  Calls on ragged
+ * multiple of 16 bytes (of a dimension longer than 1).  Token and head
+ * strides below 2^31 elements.  Calls on ragged
  * sequences have no batch dimension and do not read batch_stride.             */
 typedef struct {
     void *data;

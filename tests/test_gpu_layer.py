@@ -562,6 +562,36 @@ def test_cache_offsets_past_32_bits():
     torch.cuda.empty_cache()
 
 
+def test_strides_past_32_bits():
+    """Heads 2^30 elements apart: the third one's rows lie beyond 2^31 elements."""
+    buf = torch.zeros(2 ** 31 + 2 ** 20, dtype=torch.bfloat16, device="cuda")
+    far = 2 ** 30
+    lay = _layer(heads=3, d=128, norm="rms", page_size=16, causal_block=1, rope_dims=(128,), rope_max=(99,))
+    table = lay.ac_rope_table()
+    x = _rand(1, 20, 3, 128, seed=1)
+    want, _ = lay.ac_qk_norm_rope(x, None, table=table)
+    out = torch.as_strided(buf, (1, 3, 20, 128), (8, far, 128, 1))
+    lay.ac_qk_norm_rope(x, None, table=table, q_out=out)
+    assert torch.equal(out, want)
+    back = lay.ac_qk_norm_rope_backward(want, None, x, None, table=table)["q"]
+    assert torch.equal(lay.ac_qk_norm_rope_backward(out, None, x, None, table=table)["q"], back)
+    kp, vp, bt = _cache(lay, [40])
+    kv = torch.tensor([40], dtype=torch.int32).cuda()
+    q, near = out[0].transpose(0, 1), want[0].transpose(0, 1).contiguous()
+    buf2 = torch.zeros_like(buf)  # outputs whose span holds their input's are refused
+    for new in (3, 20):  # the kernel for few rows, and tiles
+        ref = lay.ac_cache_attn(near[:new], kp, vp, bt, _starts([new]), kv)
+        o = torch.as_strided(buf2, (new, 3, 128), (128, far, 1))
+        lay.ac_cache_attn(q[:new], kp, vp, bt, _starts([new]), kv, out=o)
+        assert torch.equal(o, ref)
+    lay.ac_cache_append(q, q, kp, vp, bt, _starts([20]), kv, table=table)
+    kp2, vp2 = kp.clone(), vp.clone()
+    lay.ac_cache_append(near, near, kp2, vp2, bt, _starts([20]), kv, table=table)
+    assert torch.equal(kp, kp2) and torch.equal(vp, vp2) and lay.get_status() == 0
+    del buf, buf2, out, q, o
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------- streams, graphs, runs
 def test_other_stream():
     lay = _layer(heads=8, d=64, page_size=16, causal_block=1, **ROPES["grid64"])

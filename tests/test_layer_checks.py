@@ -120,7 +120,8 @@ def test_norm_rope_checks(lib):
     for bad in (dict(batch=-1), dict(n=-1), dict(table=None), dict(table=base + 4), dict(qo=None), dict(q=None),
                 dict(q=_view(None, 1536, 256, 64)), dict(q=_view(base + 2, 1536, 256, 64)),
                 dict(q=_view(base, 1536, 256, 68)), dict(q=_view(base, -1536, 256, 64)),
-                dict(q=_view(base, 1 << 41, 256, 64)),
+                dict(q=_view(base, 1 << 41, 256, 64)), dict(q=_view(base, 0, 1 << 31, 64)),
+                dict(q=_view(base, 0, 256, 1 << 31)),
                 dict(qo=_view(base + 16384, 0, 64, 384)), dict(qo=_view(base + 16384, 1536, 0, 64)),
                 dict(qo=_view(base + 16384, 1536, 32, 384)), dict(qo=_view(base + 16384, 1536, 64, 128)),
                 dict(qo=_view(base + 512, 1536, 256, 64)),                        # one token further: overlaps
