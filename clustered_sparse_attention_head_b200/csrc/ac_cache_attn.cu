@@ -27,7 +27,10 @@
 //    `nsplit` runs of chunks, so that few items fill the GPU too; their sums go
 //    to the workspace unnormalised, and merge_kernel joins them.
 //
-// Bound by the tensor cores for many new tokens, by the cache's bytes for few.
+// Bound by each tile's chain softmax -> P.V -> next S (tensor pipe 63% active at
+// d = 128, 32% at d = 64, where the softmax alone takes most of it): one frame of
+// 3,600 tokens over 75,600 keys, 40 heads, d = 128: 5.1 ms, 1.09 PFLOP/s; two ragged
+// sequences of up to 2,700 tokens over 17,550 keys, 30 heads, d = 64: 852 us, 0.64.
 // Every mbarrier wait is bounded; on expiry the CTA records ST_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and returns.
 #include <algorithm>
@@ -810,8 +813,9 @@ int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStrea
     // into the number of pieces whose waves take least: a wave of pieces costs
     // their chunks plus about 3 chunks' time to start and to write out.  With
     // several sequences the items differ in length and CTAs get free at different
-    // times: then the last num_sms items or more are cut in pieces too, small
-    // enough to fill the gaps.
+    // times: then the last num_sms items or more are cut in FILL pieces too, small
+    // enough to fill the gaps (the two ragged sequences above 932 without, 863 us with
+    // 2 pieces, 845 with 4, 873 with 8; 2 keep the workspace at 79 MB).
     long long keys = a.max_kv;
     if (a.window) keys = std::min<long long>(keys, (long long)a.window + 2 * pl.tpt + a.causal_block);
     const int chunks = (int)((keys + CHUNK - 1) / CHUNK);

@@ -4,25 +4,28 @@
 // Row of a head: x [d] -> n = (x - [mean]) r, r = 1 / sqrt(mean(.^2) + eps)
 // -> n w + b -> pairs (a, b) turned by the token's angle:
 //    (a cos - b sin, a sin + b cos).
-// Bound by memory: each row is read once and written once.  A group of G lanes
-// (16 bytes each) holds one row in registers, so the statistics are xor shuffles
-// within the group.  It keeps one token and walks its heads, HC rows in flight,
-// with weight, bias, cosine and sine folded into coefficients once per token and
-// tensor: y = r (x ca + x' cb) + rb with x' the pair's other element, six
-// operations per element.
+// Bound by memory (each row is read once and written once) and, close behind it,
+// by issue slots.  A group of G lanes (16 bytes each) holds one row in registers,
+// so the statistics are xor shuffles within the group.  It takes one token at a
+// time, with weight, bias, cosine and sine folded into coefficients once for a run
+// of heads: y = r (x ca + x' cb) + rb with x' the pair's other element.
+// 75,600 tokens x 40 heads of q and k, d = 128, bf16: 501 us, 6.2 TB/s (0.94 of the
+// measured copy rate); gradients of 2 x 17,776 tokens x 30 heads, d = 64: 153 us, 5.3
+// TB/s.
 #include "ac_layer.cuh"
 #include "ac_softmax.cuh"
 
 namespace ac {
 namespace {
 
-constexpr int NT = 256;
-constexpr int FWD_HC = 8, FWD_CTAS = 3;
+constexpr int NT = 256;                  // threads of a CTA
+constexpr int FWD_HC = 8, FWD_CTAS = 3;  // heads of a run, CTAs an SM
+// heads of a step, steps of the ring, CTAs an SM, heads of a run at most
 constexpr int BACK_HC = 4, BACK_STEPS = 3, BACK_CTAS = 2, BACK_MOST = 32;
 
-// Packed pairs of fp32: one instruction for two elements.  The forward kernel
-// runs at the memory's rate only with fewer than ~170 instructions per warp and
-// 16 bytes per lane, and the scalar form took 172.
+// Packed pairs of fp32: one instruction for two elements.  The forward kernel runs
+// at the memory's rate only with fewer than ~170 instructions per warp and 16
+// bytes a lane; with layer norm the scalar form took 172, this one 140.
 typedef uint64_t f2;
 __device__ __forceinline__ f2 mul2(f2 a, f2 b) {
     f2 d;
@@ -420,13 +423,12 @@ __global__ void __launch_bounds__(NT, FWD_CTAS) norm_rope_kernel(const __grid_co
 
 // Gradients.  With n = r x (x centred): e = g' w, c = r^3 mean(e x),
 //   dx = r (e - [mean e]) - c x,  dw += (g' x) r,  db += g',
-// both means in one round of shuffles.  The CTAs take items (token tile,
-// run of heads) in turn, in steps of HC heads; a lane's own
-// g and x come through a ring of STEPS steps of cp.async copies, two steps ahead
-// (64 bytes a step and thread: the registers alone held too few loads in flight,
-// 39% of the memory's rate).  Each lane sums its elements' dw and db over all its
-// rows in registers; the CTA's sums go to part[cta] and back_sum_kernel adds the
-// CTAs in order.
+// both means in one round of shuffles.  The CTAs take items (token tile, run of
+// heads) in turn, in steps of HC heads; a lane's own g and x come through a ring of
+// STEPS steps of cp.async copies, two steps ahead (loads into registers held too
+// few in flight: 39% of DRAM's peak against 60%).  Each lane sums its elements' dw
+// and db over all its rows in registers; the CTA's sums go to part[cta] and
+// back_sum_kernel adds the CTAs in order.
 template <typename T, int D, bool HALF, bool STAT>
 __global__ void __launch_bounds__(NT, BACK_CTAS) norm_rope_back_kernel(const __grid_constant__ BackArgs a) {
     constexpr int V = Vec<T>::N, P = V / 2, G = D / V, TT = NT / G, HC = BACK_HC, STEPS = BACK_STEPS;
@@ -607,6 +609,7 @@ __global__ void __launch_bounds__(1024) back_sum_kernel(const __grid_constant__ 
     }
 }
 
+// One thread per (cos, sin) pair; once per layer.
 __global__ void rope_table_kernel(const __grid_constant__ RopeArgs r, const __grid_constant__ FreqArgs f, float2 *table,
                                   long long total) {
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
@@ -637,13 +640,15 @@ template <typename T, int D, int HC> int launch_rows(const RowArgs &a, int num_s
     if (items > 0x3fffffffLL) return -1;
     // as many rounds as the items need, and only as many CTAs as fill the rounds
     const long long rounds = (items + ctas - 1) / ctas;
-    fwd_kernel<T, D, HC>(a.rope.half, a.norm != NORM_NONE)<<<(unsigned)((items + rounds - 1) / rounds), NT, fwd_smem(HC), st>>>(
-        a, (int)runs, FastDiv((uint32_t)runs));
+    const unsigned grid = (unsigned)((items + rounds - 1) / rounds);
+    fwd_kernel<T, D, HC>(a.rope.half, a.norm != NORM_NONE)<<<grid, NT, fwd_smem(HC), st>>>(a, (int)runs,
+                                                                                        FastDiv((uint32_t)runs));
     note_launch();
     return 0;
 }
 // Runs of one head where runs of 8 would leave SMs without a CTA (few tokens): one
-// token of 40 heads 2.6 instead of 4.0 us.
+// token of 40 heads 2.5 instead of 4.1 us, 64 tokens 4.0 instead of 4.4; with 300
+// both take 5.4.
 template <typename T, int D> int launch_rows_d(const RowArgs &a, int num_sms, cudaStream_t st) {
     long long runs = 0;
     for (int i = 0; i < a.nt; i++) runs += (a.t[i].heads + FWD_HC - 1) / FWD_HC;
@@ -659,9 +664,6 @@ template <typename T, int D> BackKernel back_kernel(bool half, bool stat) {
 }
 constexpr int back_smem(bool stat) { return BACK_STEPS * (stat ? 2 : 1) * BACK_HC * NT * 16; }
 
-}  // namespace
-
-namespace {
 template <typename T, int D> int setup(int half, bool stat) {
     auto raise = [](const void *fn, int smem) {
         return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess;
@@ -699,8 +701,10 @@ int k_norm_rope_back(BackArgs &a, int dtype, int D, int num_sms, cudaStream_t st
     a.ctas[0] = h0 ? max(1, (int)((long long)total * h0 / (h0 + h1))) : 0;
     a.ctas[1] = h1 ? max(1, total - a.ctas[0]) : 0;
     const long long tt = NT / (D / (dtype == DT_BF16 ? 8 : 4)), tiles = ((long long)a.batch * a.n + tt - 1) / tt;
+    // Long runs spare the coefficients (all 30 heads 164, 8 heads 186 us on 2 x 17,776
+    // tokens); few tokens: short ones, more CTAs at work (runs of 4 / 32 heads: 64 tokens
+    // 6.6 / 17.3 us, 1,200 tokens 14.3 / 18.2).
     a.run = BACK_MOST;
-    // few tokens: shorter runs, more CTAs at work
     if (tiles * ((max(h0, h1) + a.run - 1) / a.run) < total) a.run = BACK_HC;
     for (int i = 0; i < 2; i++) {
         const int heads = a.t[i].heads;
@@ -719,9 +723,7 @@ int k_norm_rope_back(BackArgs &a, int dtype, int D, int num_sms, cudaStream_t st
                                                 : back_kernel<float, 128>(a.rope.half, stat));
     fn<<<a.ctas[0] + a.ctas[1], NT, back_smem(stat), st>>>(a);
     note_launch();
-    if (a.part) {
-        launch_after(back_sum_kernel, 4, 1024, st, a, D);
-    }
+    if (a.part) launch_after(back_sum_kernel, 4, 1024, st, a, D);
     return 0;
 }
 
