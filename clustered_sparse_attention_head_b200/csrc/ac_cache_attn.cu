@@ -362,6 +362,24 @@ __global__ void __launch_bounds__(384, 1)
                 kph ^= 1u;
             }
         };
+        // rows past the sequence's end become zeros (P is 0 there)
+        auto zero_rows = [&](unsigned char *st, int valid) {
+            for (int i = valid * 8 + lane; i < CHUNK * 8; i += 32)
+#pragma unroll
+                for (int kb = 0; kb < C::DB; kb++)
+                    *reinterpret_cast<uint4 *>(st + kb * (CHUNK * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+            fence_proxy_async_smem();
+            __syncwarp();
+        };
+        // O_t += P_t V once softmax t has written its P of phase c
+        auto pv_of = [&](int t, uint32_t c, uint64_t vdesc, bool first) -> bool {
+            ok = mbar_wait_warp(p_full + t, c & 1, abort_flag, a.status) &&
+                 (!first || act[t] == 0 || mbar_wait_warp(o_free + t, (act[t] - 1) & 1, abort_flag, a.status));
+            if (!ok) return false;
+            tc_fence_after();
+            issue_pv<D>(leader, tmem + C::TM_O + t * D, tmem + C::TM_S + t * 128, vdesc, first);
+            return true;
+        };
         auto v_next = [&]() {
             if (++vslot == C::VST) {
                 vslot = 0;
@@ -383,7 +401,6 @@ __global__ void __launch_bounds__(384, 1)
             const int nc[2] = {w.nc0, w.nc1};
             const uint64_t qd[2] = {qdesc, qdesc + (uint64_t)((w.two ? C::Q_BYTES : 0) >> 4)};
             int k_used = 0;  // K stages released in this unit
-            int v_used = 0;  // V stages waited for in this unit
 #pragma unroll
             for (int t = 0; t < 2; t++) {
                 if (t >= nt) break;
@@ -399,51 +416,58 @@ __global__ void __launch_bounds__(384, 1)
                     if (++k_used == w.nch) umma_commit_p(leader, q_empty);
                 }
             }
-            for (int j = 0; j < w.nc0 && ok; j++) {
+            if (!share) {
+                // both tiles' products of a chunk share its K and V stages; what they
+                // need besides P is waited for first, off the chain P -> P.V -> S
+                for (int j = 0; j < w.nch; j++) {
+                    const bool more = j + 1 < w.nch;
+                    if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
+                    const int valid = w.len - (w.c0 + j) * CHUNK;
+                    if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
+                    if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
+                    const uint64_t vd = vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4);
+                    const uint64_t kd = kdesc0 + (uint64_t)((kslot * C::KV_BYTES) >> 4);
 #pragma unroll
-                for (int t = 0; t < 2; t++) {
-                    if (t >= nt || j >= nc[t]) break;
-                    const uint32_t c = cnt[t] + j;
-                    if (share || t == 0) {
-                        if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
-                        // rows past the sequence's end become zeros (P is 0 there)
-                        const int valid = w.len - (w.c0 + v_used++) * CHUNK;
-                        if (valid < CHUNK) {
-                            unsigned char *st = sm + C::OFF_V + vslot * C::KV_BYTES;
-                            for (int i = valid * 8 + lane; i < CHUNK * 8; i += 32)
-#pragma unroll
-                                for (int kb = 0; kb < C::DB; kb++)
-                                    *reinterpret_cast<uint4 *>(st + kb * (CHUNK * 128) + i * 16) =
-                                        make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                            __syncwarp();
+                    for (int t = 0; t < 2; t++) {
+                        if (t >= nt) break;
+                        if (!pv_of(t, cnt[t] + j, vd, j == 0)) break;
+                        if (more) {
+                            issue_s<D>(leader, tmem + C::TM_S + t * 128, qd[t], kd);
+                            umma_commit_p(leader, s_full + t);
+                        } else {
+                            umma_commit_p(leader, o_done + t);
                         }
                     }
-                    // PV_t(j) once softmax t has written P_t(j)
-                    if (!mbar_wait_warp(p_full + t, c & 1, abort_flag, a.status)) { ok = false; break; }
-                    if (j == 0 && act[t] >= 1 && !mbar_wait_warp(o_free + t, (act[t] - 1) & 1, abort_flag, a.status)) {
-                        ok = false;
-                        break;
+                    if (!ok) break;
+                    umma_commit_p(leader, v_empty + vslot);
+                    v_next();
+                    if (more) {
+                        umma_commit_p(leader, k_empty + kslot);
+                        k_next();
+                        if (j + 2 == w.nch) umma_commit_p(leader, q_empty);
                     }
-                    tc_fence_after();
-                    issue_pv<D>(leader, tmem + C::TM_O + t * D, tmem + C::TM_S + t * 128,
-                                vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4), j == 0);
-                    if (share || t == nt - 1) {
+                }
+            } else {
+                // tile t has stages of its own: 2j + t
+                int v_used = 0;
+                for (int j = 0; j < w.nc0 && ok; j++) {
+#pragma unroll
+                    for (int t = 0; t < 2; t++) {
+                        if (j >= nc[t]) break;
+                        const bool more = j + 1 < nc[t];
+                        if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
+                        const int valid = w.len - (w.c0 + v_used++) * CHUNK;
+                        if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
+                        if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
+                        if (!pv_of(t, cnt[t] + j, vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4), j == 0)) break;
                         umma_commit_p(leader, v_empty + vslot);
                         v_next();
-                    }
-                    if (j + 1 == nc[t]) {
-                        umma_commit_p(leader, o_done + t);
-                        continue;
-                    }
-                    // S_t(j+1) into S_t, behind the P.V that reads P_t(j) from it
-                    if (share || t == 0) {
-                        if (!mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
-                        tc_fence_after();
-                    }
-                    issue_s<D>(leader, tmem + C::TM_S + t * 128, qd[t], kdesc0 + (uint64_t)((kslot * C::KV_BYTES) >> 4));
-                    umma_commit_p(leader, s_full + t);
-                    if (share || t == nt - 1) {
+                        if (!more) {
+                            umma_commit_p(leader, o_done + t);
+                            continue;
+                        }
+                        issue_s<D>(leader, tmem + C::TM_S + t * 128, qd[t], kdesc0 + (uint64_t)((kslot * C::KV_BYTES) >> 4));
+                        umma_commit_p(leader, s_full + t);
                         umma_commit_p(leader, k_empty + kslot);
                         k_next();
                         if (++k_used == w.nch) umma_commit_p(leader, q_empty);
