@@ -28,9 +28,12 @@
 //    to the workspace unnormalised, and merge_kernel joins them.
 //
 // Bound by each tile's chain softmax -> P.V -> next S (tensor pipe 63% active at
-// d = 128, 32% at d = 64, where the softmax alone takes most of it): one frame of
-// 3,600 tokens over 75,600 keys, 40 heads, d = 128: 5.1 ms, 1.09 PFLOP/s; two ragged
-// sequences of up to 2,700 tokens over 17,550 keys, 30 heads, d = 64: 852 us, 0.64.
+// d = 128, 36% at d = 64): of some 2,900 cycles a chunk takes at d = 64, a softmax
+// warp works 2,000, beside the other tile's warp for half of them, and waits 850 for
+// its next S; at d = 128 3,150, 1,800 and 1,300, at the 1.4 GHz that the power limit
+// leaves.  One frame of 3,600 tokens over 75,600 keys, 40 heads, d = 128: 5.05 ms, 1.10
+// PFLOP/s; two ragged sequences of up to 2,700 tokens over 17,550 keys, 30 heads,
+// d = 64: 770 us, 0.71.
 // Every mbarrier wait is bounded; on expiry the CTA records ST_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and returns.
 #include <algorithm>
@@ -418,7 +421,8 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!share) {
                 // both tiles' products of a chunk share its K and V stages; what they
-                // need besides P is waited for first, off the chain P -> P.V -> S
+                // need besides P is waited for first and the stages are released last, off
+                // the chain P -> P.V -> S (the two ragged sequences 857 -> 775 us)
                 for (int j = 0; j < w.nch; j++) {
                     const bool more = j + 1 < w.nch;
                     if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
@@ -838,8 +842,8 @@ int k_cache_attn(const CacheAttnArgs &a, int num_sms, void *encode_fn, cudaStrea
     // their chunks plus about 3 chunks' time to start and to write out.  With
     // several sequences the items differ in length and CTAs get free at different
     // times: then the last num_sms items or more are cut in FILL pieces too, small
-    // enough to fill the gaps (the two ragged sequences above 932 without, 863 us with
-    // 2 pieces, 845 with 4, 873 with 8; 2 keep the workspace at 79 MB).
+    // enough to fill the gaps (the two ragged sequences above 780 us without, 767 with
+    // 2 pieces, 752 with 3, 750 with 4, 777 with 8; 2 keep the workspace at 79 MB).
     long long keys = a.max_kv;
     if (a.window) keys = std::min<long long>(keys, (long long)a.window + 2 * pl.tpt + a.causal_block);
     const int chunks = (int)((keys + CHUNK - 1) / CHUNK);
