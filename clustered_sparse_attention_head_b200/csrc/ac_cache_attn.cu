@@ -594,7 +594,9 @@ __global__ void __launch_bounds__(384, 1)
                     // Move the reference max (and rescale O_t and l by f) only when it
                     // grew by more than 2^8; warp-uniform because TMEM access is
                     // collective.  PV_t(j-1) is complete: S_t(j) was issued after it.
-                    const bool rescale = j > 0 && __any_sync(0xffffffffu, m_new > m_ref + 8.f);
+                    // Rows in use alone have a say: the others hold the next sequence's
+                    // queries, or what an earlier unit left, and would decide how these round.
+                    const bool rescale = j > 0 && __any_sync(0xffffffffu, valid && m_new > m_ref + 8.f);
                     float f = 1.f;
                     if (rescale) {
                         const float m_to = fmaxf(m_ref, m_new);
