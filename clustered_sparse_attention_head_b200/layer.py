@@ -76,7 +76,11 @@ class LayerConfig:
 class AttnLayer:
     """One attention layer's calls.  ``device``: the GPU of every tensor passed
     in.  Calls that use the workspace (ac_qk_norm_rope_backward, ac_cache_attn)
-    must not overlap on the GPU with another such call of the same layer."""
+    must not overlap on the GPU with another such call of the same layer.
+
+    ``stream=`` runs a call on another stream than the current one.  Its
+    inputs must be ready there, and what it returns must be waited for before
+    it is used elsewhere (``wait_stream`` both ways); it may be freed at any time."""
 
     def __init__(self, cfg: LayerConfig, device="cuda", workspace: torch.Tensor | None = None):
         self.cfg = cfg
@@ -92,6 +96,9 @@ class AttnLayer:
         self.normed = c.norm != _abi.AC_NORM_NONE
         self.dtype, self.w_dtype = _DTYPES[cfg.dtype][1], _DTYPES[cfg.w_dtype][1]
         self._index = self.device.index
+        # allocations of these types begin from an empty tensor
+        self._f32 = torch.empty(0, dtype=torch.float32, device=self.device)
+        self._like_w = self._f32.to(self.w_dtype)
         nb = ctypes.c_size_t()
         self._pairs = 0
         if self.axes:
@@ -181,6 +188,18 @@ class AttnLayer:
             return self._plain(t, "pos", torch.int32, (batch, n, self.axes)), n * self.axes
         return self._plain(t, "pos", torch.int32, (n, self.axes)), 0
 
+    def _new(self, like, shape, stream):
+        """An uninitialised output of `like`'s type for a call on `stream`.  It is
+        allocated on that stream: a block freed on the current one may still
+        be in use there.  The current stream is recorded, so that freeing the
+        output does not hand its memory out while the caller reads it."""
+        if stream is None:
+            return like.new_empty(shape)
+        with torch.cuda.stream(stream):
+            t = like.new_empty(shape)
+        t.record_stream(torch.cuda.current_stream(self.device))
+        return t
+
     def _call(self, fn, stream, tensors, *args):
         """The C call on `stream` (default: the current stream of the layer's
         device).  Tensors used on another stream than the current one are
@@ -210,7 +229,7 @@ class AttnLayer:
         passed to the calls below."""
         if not self.axes:
             check("ac_rope_table", _abi.AC_ERR_UNSUPPORTED)
-        table = torch.empty(self._pairs, 2, dtype=torch.float32, device=self.device)
+        table = self._new(self._f32, (self._pairs, 2), stream)
         self._call("ac_rope_table", stream, (table,), table.data_ptr())
         return table
 
@@ -228,13 +247,13 @@ class AttnLayer:
         xq = yq = xk = yk = None
         if q is not None:
             if q_out is None:
-                q_out = q.new_empty((batch, self.heads, n, d))
+                q_out = self._new(q, (batch, self.heads, n, d), stream)
             xq, yq = self._bnhd(q, "q", batch, n, self.heads), self._bhnd(q_out, "q_out", batch, n, self.heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
         if k is not None:
             if k_out is None:
-                k_out = k.new_empty((batch, self.kv_heads, n, d))
+                k_out = self._new(k, (batch, self.kv_heads, n, d), stream)
             xk, yk = self._bnhd(k, "k", batch, n, self.kv_heads), self._bhnd(k_out, "k_out", batch, n, self.kv_heads)
         elif k_out is not None:
             raise ValueError("k_out without k")
@@ -255,14 +274,14 @@ class AttnLayer:
             raise ValueError("ac_qk_norm_rope_backward: gq or gk [batch, heads, n, d] is required")
         batch, n = ref.shape[0], ref.shape[2]
         pos_p, pos_stride = self._pos(pos, batch, n)
-        sums = torch.empty(4, self.d, dtype=self.w_dtype, device=self.device).unbind() if self.normed else ()
-        aq, rq = self._back_args(gq, q, w_q, b_q, dq, sums[:2], batch, n, self.heads, "q")
-        ak, rk = self._back_args(gk, k, w_k, b_k, dk, sums[2:], batch, n, self.kv_heads, "k")
+        sums = self._new(self._like_w, (4, self.d), stream).unbind() if self.normed else ()
+        aq, rq = self._back_args(gq, q, w_q, b_q, dq, sums[:2], batch, n, self.heads, "q", stream)
+        ak, rk = self._back_args(gk, k, w_k, b_k, dk, sums[2:], batch, n, self.kv_heads, "k", stream)
         self._call("ac_qk_norm_rope_backward", stream, (gq, q, w_q, *rq, gk, k, w_k, *rk, table, pos, self.ws), batch,
                    n, self._table(table), pos_p, pos_stride, *aq, *ak, self._ws_ptr, self._ws_have)
         return {"q": rq[0], "w_q": rq[1], "b_q": rq[2], "k": rk[0], "w_k": rk[1], "b_k": rk[2]}
 
-    def _back_args(self, g, x, w, b, dx, sums, batch, n, heads, name):
+    def _back_args(self, g, x, w, b, dx, sums, batch, n, heads, name, stream):
         """One tensor's arguments of the backward call, and its (dx, dw, db);
         sums: where dw and db go."""
         if g is None:
@@ -280,7 +299,7 @@ class AttnLayer:
                 self._w(b, "b_" + name)
                 db = sums[1]
         if dx is None:
-            dx = g.new_empty((batch, n, heads, self.d))
+            dx = self._new(g, (batch, n, heads, self.d), stream)
         return ((self._bhnd(g, "g" + name, batch, n, heads), xv, self._w(w, "w_" + name),
                  self._bnhd(dx, "d" + name, batch, n, heads), None if dw is None else dw.data_ptr(),
                  None if db is None else db.data_ptr()), (dx, dw, db))
@@ -311,7 +330,7 @@ class AttnLayer:
         if q is not None:
             qv = self._rows(q, "q", tokens, self.heads)
             if q_out is None:
-                q_out = q.new_empty((tokens, self.heads, self.d))
+                q_out = self._new(q, (tokens, self.heads, self.d), stream)
             qo = self._rows(q_out, "q_out", tokens, self.heads)
         elif q_out is not None:
             raise ValueError("q_out without q")
@@ -333,8 +352,8 @@ class AttnLayer:
         seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
                                                                         q_start, kv_len)
         if out is None:
-            out = q.new_empty((tokens, self.heads, self.d))
-        lse_t = torch.empty(tokens, self.heads, dtype=torch.float32, device=self.device) if lse else None
+            out = self._new(q, (tokens, self.heads, self.d), stream)
+        lse_t = self._new(self._f32, (tokens, self.heads), stream) if lse else None
         self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
                    seqs, tokens, tokens if max_q is None else int(max_q),
                    max_pages * self.cfg.page_size if max_kv is None else int(max_kv), qs, kl, bt, max_pages, num_pages,
