@@ -189,7 +189,8 @@ ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out) {
         return AC_ERR_CUDA;
     }
     cudaDriverEntryPointQueryResult qr;
-    if (cudaMemset(l->d_status, 0, 8 * sizeof(int)) != cudaSuccess ||
+    // a call on a stream that does not wait for the default one must find zeros too
+    if (cudaMemset(l->d_status, 0, 8 * sizeof(int)) != cudaSuccess || cudaStreamSynchronize(0) != cudaSuccess ||
         cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &l->encode_fn, cudaEnableDefault, &qr) != cudaSuccess ||
         qr != cudaDriverEntryPointSuccess || !l->encode_fn ||
         rope_setup(g.dtype, g.d, r.half, g.norm) || (g.page_size && g.dtype == AC_BF16 && cache_attn_setup(g.d))) {

@@ -108,6 +108,8 @@ class AttnLayer:
         self.ws_bytes = nb.value
         if workspace is None:
             workspace = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
+            # the block may still be in use on the current stream; calls may come on any
+            torch.cuda.current_stream(self.device).synchronize()
         elif workspace.device != self.device or not workspace.is_contiguous():
             raise ValueError("AttnLayer: workspace must be a contiguous tensor on the layer's device")
         self.ws = workspace

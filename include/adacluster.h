@@ -434,8 +434,9 @@ typedef struct {
 
 typedef struct ac_layer ac_layer;
 
-/* Validates the configuration and allocates the layer's status block.  *out =
- * NULL on error.                                                             */
+/* Validates the configuration and allocates the layer's status block, which is
+ * ready on every stream on return (waits for the default stream).  *out = NULL
+ * on error.                                                                  */
 AC_API ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out);
 AC_API void ac_layer_destroy(ac_layer *layer);
 
