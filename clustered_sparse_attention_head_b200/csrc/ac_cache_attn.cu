@@ -16,10 +16,12 @@
 //
 // What differs from attn3_kernel:
 //  - keys lie in pages: a lane per page reads the block table one chunk ahead
-//    and issues that page's copies; pages past the sequence's end are not read;
-//  - a chunk that runs past the sequence's end holds foreign rows (whatever the
-//    cache has there, NaN too): their scores are replaced by -inf, and the MMA
-//    warp overwrites their V rows with zeros before P.V reads them;
+//    and issues that page's copies; pages past the sequence's end, and pages wholly
+//    before the unit's lowest visible key, are not read;
+//  - a chunk that runs past the sequence's end, or begins before that key, holds
+//    foreign rows (whatever the cache or the stage has there, NaN too): their scores
+//    are replaced by -inf, and the MMA warp overwrites their V rows with zeros before
+//    P.V reads them;
 //  - each row has its own range of keys [lo, hi) (causal blocks, window); a warp
 //    masks only chunks that cross its rows' bounds, and stores zeros for chunks
 //    none of its rows sees;
@@ -94,6 +96,7 @@ struct Unit {
     int p0;          // position of the first token
     int len;         // the sequence's keys
     int c0, nch;     // chunks of this unit
+    int lo;          // lowest key that any of its tokens sees
     int slot;        // partial slot, or -1: whole
     int nt;          // tiles at work
     bool two;        // two tiles of rows (else both tiles share one)
@@ -118,13 +121,13 @@ __device__ __forceinline__ Unit decode(const CacheAttnArgs &a, const Plan &pl, i
     w.row0 += t0;
     w.p0 += t0;
     w.nq = max(0, min(2 * pl.tpt, w.nq - t0));
-    w.c0 = w.nch = 0;
+    w.c0 = w.nch = w.lo = 0;
     if (w.nq) {
-        int lo, hi, x;
-        key_range(a, w.p0, w.len, lo, x);
+        int hi, x;
+        key_range(a, w.p0, w.len, w.lo, x);
         key_range(a, w.p0 + w.nq - 1, w.len, x, hi);
-        if (hi > lo) {
-            const int first = lo / CHUNK, all = (hi + CHUNK - 1) / CHUNK - first;
+        if (hi > w.lo) {
+            const int first = w.lo / CHUNK, all = (hi + CHUNK - 1) / CHUNK - first;
             const int np = w.slot < 0 ? 1 : pl.nsplit, per = (all + np - 1) / np;
             w.c0 = first + piece * per;
             w.nch = max(0, min(per, all - piece * per));
@@ -307,10 +310,11 @@ __global__ void __launch_bounds__(384, 1)
                 qi++;
             }
             const int32_t *table = a.block_table + (long long)w.s * a.max_pages;
-            // rows of the pool where chunk c's page `lane` begins; -1: none
+            // rows of the pool where chunk c's page `lane` begins; -1: none (past the
+            // end, or before every window: such a page may have been given back)
             auto page_row = [&](int c) -> int {
                 const int j = c * CHUNK + lane * box;
-                if (lane * box >= CHUNK || j >= w.len) return -1;
+                if (lane * box >= CHUNK || j >= w.len || j + box <= w.lo) return -1;
                 int id = __ldg(table + (j >> a.page_log2));
                 if (id < 0 || id >= a.num_pages) {
                     set_status(a.status, ST_INVALID);
@@ -365,9 +369,11 @@ __global__ void __launch_bounds__(384, 1)
                 kph ^= 1u;
             }
         };
-        // rows past the sequence's end become zeros (P is 0 there)
-        auto zero_rows = [&](unsigned char *st, int valid) {
-            for (int i = valid * 8 + lane; i < CHUNK * 8; i += 32)
+        const int box = min(1 << a.page_log2, CHUNK);
+        // rows that were not loaded, past the sequence's end or before every window,
+        // become zeros (P is 0 there)
+        auto zero_rows = [&](unsigned char *st, int from, int to) {
+            for (int i = from * 8 + lane; i < to * 8; i += 32)
 #pragma unroll
                 for (int kb = 0; kb < C::DB; kb++)
                     *reinterpret_cast<uint4 *>(st + kb * (CHUNK * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -404,6 +410,8 @@ __global__ void __launch_bounds__(384, 1)
             const int nc[2] = {w.nc0, w.nc1};
             const uint64_t qd[2] = {qdesc, qdesc + (uint64_t)((w.two ? C::Q_BYTES : 0) >> 4)};
             int k_used = 0;  // K stages released in this unit
+            // rows of the first chunk on pages before every window
+            const int front = (w.lo & ~(box - 1)) - w.c0 * CHUNK;
 #pragma unroll
             for (int t = 0; t < 2; t++) {
                 if (t >= nt) break;
@@ -427,7 +435,8 @@ __global__ void __launch_bounds__(384, 1)
                     const bool more = j + 1 < w.nch;
                     if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
                     const int valid = w.len - (w.c0 + j) * CHUNK;
-                    if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
+                    if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid, CHUNK);
+                    if (j == 0 && front > 0) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, 0, front);
                     if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
                     const uint64_t vd = vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4);
                     const uint64_t kd = kdesc0 + (uint64_t)((kslot * C::KV_BYTES) >> 4);
@@ -461,7 +470,8 @@ __global__ void __launch_bounds__(384, 1)
                         const bool more = j + 1 < nc[t];
                         if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
                         const int valid = w.len - (w.c0 + v_used++) * CHUNK;
-                        if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
+                        if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid, CHUNK);
+                        if (j == 0 && t == 0 && front > 0) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, 0, front);
                         if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
                         if (!pv_of(t, cnt[t] + j, vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4), j == 0)) break;
                         umma_commit_p(leader, v_empty + vslot);

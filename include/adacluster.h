@@ -522,8 +522,10 @@ AC_API ac_status ac_cache_append(ac_layer *layer, int seqs, int tokens, const in
  * sequence: a sequence beyond its bound, or beyond the block table, is cut to
  * it (its first max_q new tokens, its first max_kv keys) and AC_ERR_INVALID_ARG
  * recorded; a page id outside the pool is clamped and recorded.  Cache rows at
- * or beyond kv_len are never used, whatever they hold; rows before it must be
- * finite (a NaN or Inf value may reach every query of its sequence).
+ * or beyond kv_len are never used, whatever they hold, nor are block table
+ * entries (and pages) wholly before the lowest key that the window leaves to any
+ * new token of the sequence; all other rows must be finite (a NaN or Inf value may
+ * reach every query of its sequence).
  * max_q = 0: no sequence has new tokens, nothing is written.  At most 128 query
  * heads per key head, and no broadcast q (a stride of 0): AC_ERR_UNSUPPORTED.
  * bf16 only (AC_ERR_UNSUPPORTED otherwise): products in bf16 with fp32
