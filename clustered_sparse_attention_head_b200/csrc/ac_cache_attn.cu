@@ -20,8 +20,8 @@
 //    before the unit's lowest visible key, are not read;
 //  - a chunk that runs past the sequence's end, or begins before that key, holds
 //    foreign rows (whatever the cache or the stage has there, NaN too): their scores
-//    are replaced by -inf, and the MMA warp overwrites their V rows with zeros before
-//    P.V reads them;
+//    are replaced by -inf, and the MMA warp (past the end) or the V producer (before that
+//    key) overwrites their V rows with zeros before P.V reads them;
 //  - each row has its own range of keys [lo, hi) (causal blocks, window); a warp
 //    masks only chunks that cross its rows' bounds, and stores zeros for chunks
 //    none of its rows sees;
@@ -170,6 +170,17 @@ __device__ __forceinline__ void tma_load_3d_hint_p(uint32_t leader, void *dst, c
         "[%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(smem_u32(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "l"(policy), "r"(leader)
         : "memory");
+}
+
+// Rows [from, to) of a V stage become zeros, for the MMAs issued after a barrier
+// that the calling warp arrives on next.
+template <int D> __device__ __forceinline__ void zero_rows(unsigned char *st, int from, int to, int lane) {
+    for (int i = from * 8 + lane; i < to * 8; i += 32)
+#pragma unroll
+        for (int kb = 0; kb < CCfg<D>::DB; kb++)
+            *reinterpret_cast<uint4 *>(st + kb * (CHUNK * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
 template <int D>
@@ -332,6 +343,10 @@ __global__ void __launch_bounds__(384, 1)
                     break;
                 }
                 const int pages = __popc(__ballot_sync(0xffffffffu, row >= 0));
+                // pages before every window, at the front of the unit's first chunk: P is
+                // 0 there and V must be too (off the MMA warp's chain: 5.22 against 5.31 ms)
+                const int front = kq ? 0 : (w.lo & ~(box - 1)) - (w.c0 + c) * CHUNK;
+                if (front > 0) zero_rows<D>(ring + slot * C::KV_BYTES, 0, front, lane);
                 mbar_arrive_expect_tx_p(leader, full + slot, (uint32_t)(pages * box * 128 * C::DB));
                 __syncwarp();
 #pragma unroll
@@ -369,17 +384,8 @@ __global__ void __launch_bounds__(384, 1)
                 kph ^= 1u;
             }
         };
-        const int box = min(1 << a.page_log2, CHUNK);
-        // rows that were not loaded, past the sequence's end or before every window,
-        // become zeros (P is 0 there)
-        auto zero_rows = [&](unsigned char *st, int from, int to) {
-            for (int i = from * 8 + lane; i < to * 8; i += 32)
-#pragma unroll
-                for (int kb = 0; kb < C::DB; kb++)
-                    *reinterpret_cast<uint4 *>(st + kb * (CHUNK * 128) + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-            fence_proxy_async_smem();
-            __syncwarp();
-        };
+        // rows past the sequence's end become zeros (P is 0 there)
+        auto zero_tail = [&](unsigned char *st, int valid) { zero_rows<D>(st, valid, CHUNK, lane); };
         // O_t += P_t V once softmax t has written its P of phase c
         auto pv_of = [&](int t, uint32_t c, uint64_t vdesc, bool first) -> bool {
             ok = mbar_wait_warp(p_full + t, c & 1, abort_flag, a.status) &&
@@ -410,8 +416,6 @@ __global__ void __launch_bounds__(384, 1)
             const int nc[2] = {w.nc0, w.nc1};
             const uint64_t qd[2] = {qdesc, qdesc + (uint64_t)((w.two ? C::Q_BYTES : 0) >> 4)};
             int k_used = 0;  // K stages released in this unit
-            // rows of the first chunk on pages before every window
-            const int front = (w.lo & ~(box - 1)) - w.c0 * CHUNK;
 #pragma unroll
             for (int t = 0; t < 2; t++) {
                 if (t >= nt) break;
@@ -435,8 +439,7 @@ __global__ void __launch_bounds__(384, 1)
                     const bool more = j + 1 < w.nch;
                     if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
                     const int valid = w.len - (w.c0 + j) * CHUNK;
-                    if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid, CHUNK);
-                    if (j == 0 && front > 0) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, 0, front);
+                    if (valid < CHUNK) zero_tail(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
                     if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
                     const uint64_t vd = vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4);
                     const uint64_t kd = kdesc0 + (uint64_t)((kslot * C::KV_BYTES) >> 4);
@@ -470,8 +473,7 @@ __global__ void __launch_bounds__(384, 1)
                         const bool more = j + 1 < nc[t];
                         if (!mbar_wait_warp(v_full + vslot, vph, abort_flag, a.status)) { ok = false; break; }
                         const int valid = w.len - (w.c0 + v_used++) * CHUNK;
-                        if (valid < CHUNK) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, valid, CHUNK);
-                        if (j == 0 && t == 0 && front > 0) zero_rows(sm + C::OFF_V + vslot * C::KV_BYTES, 0, front);
+                        if (valid < CHUNK) zero_tail(sm + C::OFF_V + vslot * C::KV_BYTES, valid);
                         if (more && !mbar_wait_warp(k_full + kslot, kph, abort_flag, a.status)) { ok = false; break; }
                         if (!pv_of(t, cnt[t] + j, vdesc0 + (uint64_t)((vslot * C::KV_BYTES) >> 4), j == 0)) break;
                         umma_commit_p(leader, v_empty + vslot);
