@@ -374,6 +374,7 @@ ac_status ac_cache_append(ac_layer *l, int seqs, int tokens, const int32_t *q_st
     memset(&a, 0, sizeof(a));
     const ac_status re = rope_of(l, table, pos, 0, 1, a.rope);
     if (re != AC_OK) return re;
+    a.rope.line = a.rope.axes == 1;
     const int d = l->cfg.d, hk = l->cfg.kv_heads, hq = l->cfg.heads;
     if (tokens) {
         if (!view_ok(*k, 1, tokens, hk, d, l->elt, false) || !view_ok(*v, 1, tokens, hk, d, l->elt, false))

@@ -35,6 +35,7 @@ struct RopeArgs {
     int max[3];           // positions of each axis
     uint32_t off[3];      // first (cos, sin) of each axis in the table
     int cells;            // product of max, at most 2^31 - 1: tokens of the implicit grid
+    int line;             // 1: the implicit tokens are a stream of one axis, recorded at or beyond cells
     FastDiv by1, by2;     // by max[1] and max[2]
     const float2 *table;
     const int32_t *pos;   // NULL: row-major coordinates of the token's index

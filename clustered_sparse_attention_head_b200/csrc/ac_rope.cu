@@ -116,7 +116,10 @@ __device__ __forceinline__ bool token_pos(const RopeArgs &r, long long at, int i
     p[0] = p[1] = p[2] = 0;
     if (r.axes == 0) return false;
     if (!r.pos) {
-        if (index >= r.cells) return false;
+        if (index >= r.cells) {
+            if (r.line) set_status(status, ST_INVALID);
+            return false;
+        }
         if (r.axes == 1) {
             p[0] = index;
         } else if (r.axes == 2) {

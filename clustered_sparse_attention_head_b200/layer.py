@@ -323,7 +323,8 @@ class AttnLayer:
                         w_q=None, w_k=None, b_q=None, b_k=None, q_out=None, stream=None):
         """Writes the new tokens' keys (normed, rotated) and values [tokens,
         kv_heads, d] to their pages; with q [tokens, heads, d] returns the normed
-        and rotated queries (q_out if given), else None."""
+        and rotated queries (q_out if given), else None.  On one axis without
+        pos, tokens past the table stay unrotated and set the status word."""
         tokens = k.shape[0]
         seqs, _, qs, kl, bt, max_pages, num_pages, kp, vp = self._cache(tokens, k_pages, v_pages, block_table,
                                                                         q_start, kv_len)

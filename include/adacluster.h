@@ -502,7 +502,10 @@ AC_API ac_status ac_qk_norm_rope_backward(ac_layer *layer, int batch, int n, con
  * ac_qk_norm_rope, and values to their places in the pools, and (q non-NULL)
  * the queries, normed and turned, to q_out, in one launch.  A token's position
  * is its place in the sequence, read as in ac_qk_norm_rope with pos = NULL, or
- * pos [tokens, rope_axes].  A token whose page id is outside [0, num_pages) or
+ * pos [tokens, rope_axes].  With pos = NULL and one axis, a token at or beyond
+ * rope_max[0] (a sequence that outgrew its table) is written unrotated and
+ * recorded (AC_ERR_INVALID_ARG); behind a grid of several axes such tokens are
+ * text, so a clip that may outgrow its grid passes pos.  A token whose page id is outside [0, num_pages) or
  * whose place is outside the block table is not written to the cache, and
  * AC_ERR_INVALID_ARG is recorded.  Two sequences that share a page being
  * written race for it.                                                        */
