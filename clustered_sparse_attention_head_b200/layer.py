@@ -26,6 +26,11 @@ _DTYPES = {"bf16": (_abi.AC_BF16, torch.bfloat16), "f32": (_abi.AC_F32, torch.fl
 _view = struct.Struct("Qqqq").pack  # an ac_tensor as bytes, which ctypes passes by address
 
 
+def _int32(v):
+    """A bound as a C int, which ctypes would take modulo 2^32."""
+    return min(max(int(v), -1 << 31), (1 << 31) - 1)
+
+
 @dataclass
 class LayerConfig:
     heads: int
@@ -61,6 +66,10 @@ class LayerConfig:
 
         if len(self.rope_dims) != len(self.rope_max) or len(self.rope_dims) > 3:
             raise ValueError("LayerConfig: rope_dims and rope_max take one number per axis, at most three")
+        for name in ("heads", "kv_heads", "d", "rope_dims", "rope_max", "rope_orig", "page_size", "causal_block", "window"):
+            v = getattr(self, name)
+            if any(_int32(x) != x for x in (v if name in ("rope_dims", "rope_max") else (v,))):
+                raise ValueError(f"LayerConfig: {name} must be 32-bit integers, not {v!r}")
         dims = (ctypes.c_int * 3)(*self.rope_dims)
         top = (ctypes.c_int * 3)(*self.rope_max)
         return _abi.ac_layer_config(
@@ -358,8 +367,8 @@ class AttnLayer:
             out = self._new(q, (tokens, self.heads, self.d), stream)
         lse_t = self._new(self._f32, (tokens, self.heads), stream) if lse else None
         self._call("ac_cache_attn", stream, (q, k_pages, v_pages, block_table, q_start, kv_len, out, lse_t, self.ws),
-                   seqs, tokens, tokens if max_q is None else int(max_q),
-                   max_pages * self.cfg.page_size if max_kv is None else int(max_kv), qs, kl, bt, max_pages, num_pages,
+                   seqs, tokens, tokens if max_q is None else _int32(max_q),
+                   _int32(max_pages * self.cfg.page_size if max_kv is None else max_kv), qs, kl, bt, max_pages, num_pages,
                    self._rows(q, "q", tokens, self.heads), kp, vp, self._rows(out, "out", tokens, self.heads),
                    None if lse_t is None else lse_t.data_ptr(),
                    self._ws_ptr, self._ws_have)
