@@ -429,8 +429,10 @@ ac_status ac_cache_attn(ac_layer *l, int seqs, int tokens, int max_q, int max_kv
     a.seqs = seqs;
     a.tokens = tokens;
     a.max_q = std::min(max_q, tokens);
-    // no page can hold a key beyond these
-    a.max_kv = num_pages ? (int)std::min<long long>(max_kv, (long long)max_pages * l->cfg.page_size) : 0;
+    // no page can hold a key beyond these; the end of a chunk or tile of keys that
+    // begins below MAX_KEYS is a 32-bit number too
+    constexpr int MAX_KEYS = 0x7fff0000;
+    a.max_kv = num_pages ? (int)std::min<long long>(std::min(max_kv, MAX_KEYS), (long long)max_pages * l->cfg.page_size) : 0;
     a.heads = hq;
     a.kv_heads = l->cfg.kv_heads;
     a.group = hq / l->cfg.kv_heads;

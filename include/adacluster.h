@@ -523,8 +523,8 @@ AC_API ac_status ac_cache_append(ac_layer *layer, int seqs, int tokens, const in
  * heads] (natural-log log-sum-exp of the scaled scores) is written when
  * non-NULL.  max_q and max_kv bound the new tokens and the length of any
  * sequence: a sequence beyond its bound, or beyond the block table, is cut to
- * it (its first max_q new tokens, its first max_kv keys) and AC_ERR_INVALID_ARG
- * recorded; a page id outside the pool is clamped and recorded.  Cache rows at
+ * it (its first max_q new tokens, its first max_kv keys, of 2^31 - 2^16 at most)
+ * and AC_ERR_INVALID_ARG recorded; a page id outside the pool is clamped and recorded.  Cache rows at
  * or beyond kv_len are never used, whatever they hold, nor are block table
  * entries (and pages) wholly before the lowest key that the window leaves to any
  * new token of the sequence; all other rows must be finite (a NaN or Inf value may
