@@ -82,6 +82,39 @@ class LayerConfig:
             float(self.scale))
 
 
+class _NormRope(torch.autograd.Function):
+    """ac_qk_norm_rope in torch's graph: ac_qk_norm_rope_backward on the way back."""
+
+    @staticmethod
+    def forward(ctx, layer, table, pos, stream, q, k, w_q, w_k, b_q, b_k):
+        ctx.layer = layer
+        ctx.set_materialize_grads(False)
+        x = (q, k, w_q, w_k, b_q, b_k) if layer.normed else (None,) * 6  # a rotation's gradient needs none of them
+        ctx.save_for_backward(table, pos, *x)
+        return layer.ac_qk_norm_rope(q, k, table, pos, w_q, w_k, b_q, b_k, stream=stream)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, gq, gk):
+        table, pos, q, k, w_q, w_k, b_q, b_k = ctx.saved_tensors
+        need = ctx.needs_input_grad[4:]
+        gq = gq if need[0] or need[2] or need[4] else None
+        gk = gk if need[1] or need[3] or need[5] else None
+        if gq is None and gk is None:
+            return (None,) * 10
+        r = ctx.layer.ac_qk_norm_rope_backward(_readable(gq), _readable(gk), q, k, table, pos, w_q, w_k, b_q, b_k)
+        return (None,) * 4 + tuple(r[n] for n in ("q", "k", "w_q", "w_k", "b_q", "b_k"))
+
+
+def _readable(g):
+    """A gradient whose strides and alignment the calls take: torch hands on
+    any, a sum's with strides of 0 among them."""
+    if g is None or (g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and
+                     all(s * g.element_size() % 16 == 0 and s < 1 << 31 for s in g.stride()[:-1])):
+        return g
+    return g.clone(memory_format=torch.contiguous_format)
+
+
 class AttnLayer:
     """One attention layer's calls.  ``device``: the GPU of every tensor passed
     in.  Calls that use the workspace (ac_qk_norm_rope_backward, ac_cache_attn)
@@ -250,7 +283,14 @@ class AttnLayer:
         (views of any strides; either may be None).  Returns (q_out, k_out) in
         the attention's layout [batch, heads, n, d] unless given; given outputs
         are [batch, heads, n, d] views too, and q_out = q.transpose(1, 2) works
-        in place."""
+        in place.  Under autograd the outputs carry the gradients of
+        ac_qk_norm_rope_backward to inputs, weights and biases that ask for them
+        (given outputs cannot; the cache's calls have no gradients)."""
+        if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, w_q, w_k, b_q, b_k)):
+            if q_out is not None or k_out is not None:
+                raise ValueError("ac_qk_norm_rope: q_out and k_out do not join torch's graph, but an input requires a "
+                                 "gradient; call it under torch.no_grad()")
+            return _NormRope.apply(self, table, pos, stream, q, k, w_q, w_k, b_q, b_k)
         ref = q if q is not None else k
         if ref is None or ref.dim() != 4:
             raise ValueError("ac_qk_norm_rope: q or k [batch, n, heads, d] is required")
