@@ -33,9 +33,9 @@
 // d = 128, 36% at d = 64): of some 2,900 cycles a chunk takes at d = 64, a softmax
 // warp works 2,000, beside the other tile's warp for half of them, and waits 850 for
 // its next S; at d = 128 3,150, 1,800 and 1,300, at the 1.4 GHz that the power limit
-// leaves.  One frame of 3,600 tokens over 75,600 keys, 40 heads, d = 128: 5.05 ms, 1.10
-// PFLOP/s; two ragged sequences of up to 2,700 tokens over 17,550 keys, 30 heads,
-// d = 64: 770 us, 0.71.
+// leaves.  One frame of 3,600 tokens over 75,600 keys, 40 heads, d = 128: 4.97 to 5.24 ms
+// on several B200s, 1.12 to 1.06 PFLOP/s; two ragged sequences of up to 2,700 tokens
+// over 17,550 keys, 30 heads, d = 64: 774 to 826 us, 0.71 to 0.66.
 // Every mbarrier wait is bounded; on expiry the CTA records ST_TIMEOUT, drains
 // its copies and MMAs, frees TMEM and returns.
 #include <algorithm>

@@ -9,9 +9,10 @@
 // so the statistics are xor shuffles within the group.  It takes one token at a
 // time, with weight, bias, cosine and sine folded into coefficients once for a run
 // of heads: y = r (x ca + x' cb) + rb with x' the pair's other element.
-// 75,600 tokens x 40 heads of q and k, d = 128, bf16: 501 us, 6.2 TB/s (0.94 of the
-// measured copy rate); gradients of 2 x 17,776 tokens x 30 heads, d = 64: 153 us, 5.3
-// TB/s.
+// 75,600 tokens x 40 heads of q and k, d = 128, bf16: 502 to 559 us on several B200s, 6.2 to
+// 5.5 TB/s (0.94 to 0.84 of the measured copy rate; the faster end leaves the last of
+// the output in L2); gradients of 2 x 17,776 tokens x 30 heads, d = 64: 153 to 168 us,
+// 5.3 to 4.9 TB/s.
 #include "ac_layer.cuh"
 #include "ac_softmax.cuh"
 

@@ -373,7 +373,9 @@ AC_API const char *ac_status_string(ac_status s);
  *    block table) is read from device memory.
  * ------------------------------------------------------------------------ */
 
-/* Norm of each head's d elements before weight w and bias b [d]:
+/* Norm of each head's d elements before weight w and bias b [d] (a model that
+ * norms all heads of a projected row together, with a weight of heads x d, does
+ * so itself and takes NONE):
  *   RMS:   y = x / sqrt(mean(x^2) + eps) * w + b
  *   LAYER: the same of x - mean(x)
  *   NONE:  y = x (w and b are not used).                                    */
@@ -392,7 +394,11 @@ typedef enum { AC_NORM_NONE = 0, AC_NORM_RMS = 1, AC_NORM_LAYER = 2 } ac_norm;
  *           turns within the original context of `orig` positions; cosine and
  *           sine are multiplied by 0.1 ln(factor) + 1
  *           ("YaRN: Efficient Context Window Extension of Large Language
- *           Models", Peng et al., arXiv 2309.00071, §3).                     */
+ *           Models", Peng et al., arXiv 2309.00071, §3).  The ramp is linear
+ *           in the turns, as there; code in use often ramps linearly over
+ *           the pair's index j between two rounded bounds instead, and
+ *           weights tuned with that expect other frequencies for the pairs
+ *           between the bounds.                                            */
 typedef enum { AC_ROPE_INTERLEAVED = 0, AC_ROPE_HALF = 1 } ac_rope_layout;
 typedef enum { AC_ROPE_PLAIN = 0, AC_ROPE_LINEAR = 1, AC_ROPE_NTK = 2, AC_ROPE_YARN = 3 } ac_rope_scaling;
 
@@ -464,9 +470,11 @@ AC_API ac_status ac_rope_table(ac_layer *layer, float *table, void *stream);
  * row-major coordinates of i in the grid rope_max[0] x rope_max[1] x ..., and
  * tokens behind the grid (text) are not rotated.
  * q / q_out or k / k_out may both be NULL (that side is skipped).  w and b may
- * be NULL (1 and 0).  An output may be its input (same data and strides) and
- * must not overlap an input otherwise.  Statistics and rotation in fp32, one
- * rounding at the end.                                                        */
+ * be NULL (1 and 0).  An output may be its input (same data and strides);
+ * otherwise the memory from its first to its last element must lie apart from
+ * its input's (AC_ERR_INVALID_ARG: also for two slices of one packed buffer).  It
+ * must share no element with the other tensor's input or output (not checked).
+ * Statistics and rotation in fp32, one rounding at the end.                   */
 AC_API ac_status ac_qk_norm_rope(ac_layer *layer, int batch, int n, const float *table, const int32_t *pos,
                                  int64_t pos_batch_stride, const ac_tensor *q, const void *w_q, const void *b_q,
                                  const ac_tensor *q_out, const ac_tensor *k, const void *w_k, const void *b_k,
