@@ -122,7 +122,10 @@ class AttnLayer:
 
     ``stream=`` runs a call on another stream than the current one.  Its
     inputs must be ready there, and what it returns must be waited for before
-    it is used elsewhere (``wait_stream`` both ways); it may be freed at any time."""
+    it is used elsewhere (``wait_stream`` both ways); it may be freed at any time.
+
+    A CUDA graph that captured calls writes to the layer's status block and
+    workspace: keep the layer for as long as the graph."""
 
     def __init__(self, cfg: LayerConfig, device="cuda", workspace: torch.Tensor | None = None):
         self.cfg = cfg

@@ -444,6 +444,8 @@ typedef struct ac_layer ac_layer;
  * ready on every stream on return (waits for the default stream).  *out = NULL
  * on error.                                                                  */
 AC_API ac_status ac_layer_create(const ac_layer_config *cfg, ac_layer **out);
+/* Frees the layer's device memory, after the device's work.  A CUDA graph that
+ * captured the layer's calls writes to that memory: destroy the graph first. */
 AC_API void ac_layer_destroy(ac_layer *layer);
 
 /* Bytes of workspace for the calls below that take one (one size for all). */
